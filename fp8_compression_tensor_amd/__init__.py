@@ -22,12 +22,17 @@ __all__ = [
     "compress", "decompress", "reduce_fp8", "compress_raw", "decompress_raw", "reduce_fp8_raw",
     "status_string", "lib", "LIB_PATH", "TFP8Error", "BF16", "F32", "SUPPORTED_BLOCKS",
     "FLAG_INT8", "FLAG_NO_ROTATION", "accumulate", "accumulate_raw", "reduce_strided_raw",
+    "compress_t", "matmul", "matmul_grouped", "matmul_grouped_t", "padded_rows",
+    "compress_t_raw", "matmul_raw", "matmul_grouped_raw", "matmul_grouped_t_raw",
+    "PRODUCT_BLOCKS", "MAX_GROUPS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtfp8.so")
 BF16, F32 = 0, 1
 FLAG_INT8, FLAG_NO_ROTATION = 1, 2  # variant flags of the *_ex entry points (include/tfp8.h)
 SUPPORTED_BLOCKS = (64, 128, 256, 512)
+PRODUCT_BLOCKS = (128, 256, 512)  # blocks that the products of compressed operands take
+MAX_GROUPS = 65536
 
 _STATUS = {0: "TFP8_OK", -1: "TFP8_E_NULL", -2: "TFP8_E_SIZE", -3: "TFP8_E_BLOCK",
            -4: "TFP8_E_DTYPE", -5: "TFP8_E_ALIGN", -6: "TFP8_E_ARG", -7: "TFP8_E_HIP"}
@@ -65,6 +70,19 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.tfp8_reduce_strided.restype = i32
     L.tfp8_accumulate.argtypes = [vp, vp, vp, vp, i32, i64, i32, f32, u32, vp, vp, vp, vp]
     L.tfp8_accumulate.restype = i32
+    L.tfp8_padded_rows.argtypes = [i64, i32, i32]
+    L.tfp8_padded_rows.restype = i64
+    L.tfp8_compress_t.argtypes = [vp, i32, i64, i64, i64, vp, i32, i32, f32, u32, vp, vp, vp, vp]
+    L.tfp8_compress_t.restype = i32
+    operand = [vp, i64, vp, vp, i64]
+    L.tfp8_matmul.argtypes = [*operand, *operand, i64, i64, i64, i32, vp, i32, i64, vp]
+    L.tfp8_matmul.restype = i32
+    L.tfp8_matmul_grouped.argtypes = [*operand, *operand, vp, i32, i64, i64, i64, i32, vp, i32,
+                                      i64, vp]
+    L.tfp8_matmul_grouped.restype = i32
+    L.tfp8_matmul_grouped_t.argtypes = [*operand, *operand, vp, i32, i64, i64, i64, i32, vp, i32,
+                                        vp]
+    L.tfp8_matmul_grouped_t.restype = i32
     L.tfp8_status_string.argtypes = [i32]
     L.tfp8_status_string.restype = ctypes.c_char_p
     L.tfp8_version.argtypes = []
@@ -138,6 +156,33 @@ def accumulate_raw(codes_ptr: int, alpha_ptr: int, scale_ptr: int, grad_ptr: int
                    scale_out_ptr: int, stream: int = 0, flags: int = 0) -> int:
     return lib().tfp8_accumulate(codes_ptr, alpha_ptr, scale_ptr, grad_ptr, grad_dtype, n, block,
                                  target, flags, codes_out_ptr, alpha_out_ptr, scale_out_ptr, stream)
+
+
+def compress_t_raw(x_ptr: int, x_dtype: int, rows: int, cols: int, ldx: int, offsets_ptr,
+                   groups: int, block: int, target: float, codes_ptr: int, alpha_ptr: int,
+                   scale_ptr: int, stream: int = 0, flags: int = 0) -> int:
+    return lib().tfp8_compress_t(x_ptr, x_dtype, rows, cols, ldx, offsets_ptr, groups, block,
+                                 target, flags, codes_ptr, alpha_ptr, scale_ptr, stream)
+
+
+# An operand of a product is (codes_ptr, ld, alpha_ptr, scale_ptr, lds): row strides in codes and
+# in scales.
+
+def matmul_raw(a, b, m: int, n: int, k: int, block: int, out_ptr: int, out_dtype: int, ldc: int,
+               stream: int = 0) -> int:
+    return lib().tfp8_matmul(*a, *b, m, n, k, block, out_ptr, out_dtype, ldc, stream)
+
+
+def matmul_grouped_raw(a, b, offsets_ptr: int, groups: int, m: int, n: int, k: int, block: int,
+                       out_ptr: int, out_dtype: int, ldc: int, stream: int = 0) -> int:
+    return lib().tfp8_matmul_grouped(*a, *b, offsets_ptr, groups, m, n, k, block, out_ptr,
+                                     out_dtype, ldc, stream)
+
+
+def matmul_grouped_t_raw(a, b, offsets_ptr: int, groups: int, rows: int, m: int, n: int,
+                         block: int, out_ptr: int, out_dtype: int, stream: int = 0) -> int:
+    return lib().tfp8_matmul_grouped_t(*a, *b, offsets_ptr, groups, rows, m, n, block, out_ptr,
+                                       out_dtype, stream)
 
 
 # ---------------------------------------------------------------------------- tensor wrappers
@@ -331,4 +376,215 @@ def accumulate(codes: torch.Tensor, alpha: torch.Tensor, scale: torch.Tensor, gr
         _check(accumulate_raw(codes.data_ptr(), alpha.data_ptr(), scale.data_ptr(),
                               grad.data_ptr(), dt, n, block, float(target), out[0].data_ptr(),
                               out[1].data_ptr(), out[2].data_ptr(), _stream(codes), flags))
+    return out
+
+
+# ------------------------------------------------------------- products of compressed operands
+
+def padded_rows(rows: int, groups: int = 1, block: int = 128) -> int:
+    """Length of a compress_t row: room for `rows` rows in `groups` groups, each rounded up to a
+    whole block, whatever the sizes of the groups."""
+    if rows < 0 or not 1 <= groups <= MAX_GROUPS or block < 1:
+        raise ValueError(f"padded_rows({rows}, {groups}, {block}): out of range")
+    return (rows + groups * (block - 1)) // block * block
+
+
+def _product_block(block: int):
+    if block not in PRODUCT_BLOCKS:
+        raise ValueError(f"block must be one of {PRODUCT_BLOCKS}, got {block}")
+
+
+def _out_dtype(dtype: torch.dtype) -> int:
+    if dtype == torch.float32:
+        return F32
+    if dtype == torch.bfloat16:
+        return BF16
+    raise ValueError(f"unsupported output dtype {dtype}")
+
+
+def _offsets_of(offsets: torch.Tensor, device: torch.device) -> int:
+    """The number of groups that offsets cut."""
+    if not (isinstance(offsets, torch.Tensor) and offsets.is_cuda):
+        raise ValueError("tfp8 operates on GPU tensors only (no CPU path)")
+    if offsets.device != device:
+        raise ValueError(f"tensors on different devices ({device} and {offsets.device})")
+    if offsets.dtype != torch.int64 or offsets.dim() != 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int64 vector")
+    groups = offsets.numel() - 1
+    if not 1 <= groups <= MAX_GROUPS:
+        raise ValueError(f"offsets must have 2 to {MAX_GROUPS + 1} elements, got {groups + 1}")
+    return groups
+
+
+def _operand(t, block: int, dims: int, name: str):
+    """(codes, alpha, scale) of an operand -> (shape of codes, its raw form, device).
+
+    codes is uint8 [rows, k] (dims = 2, rows at any stride that is a multiple of 16) or contiguous
+    [groups, rows, k]; alpha and scale are float32 with k / block values a row, [rows, k / block]
+    with contiguous rows, or contiguous in any shape (as compress returns them)."""
+    codes, alpha, scale = t
+    for x, dt, what in ((codes, torch.uint8, "codes"), (alpha, torch.float32, "alpha"),
+                        (scale, torch.float32, "scale")):
+        if not (isinstance(x, torch.Tensor) and x.is_cuda):
+            raise ValueError("tfp8 operates on GPU tensors only (no CPU path)")
+        if x.dtype != dt:
+            raise ValueError(f"{what} of {name} must be {dt}, got {x.dtype}")
+        if x.device != codes.device:
+            raise ValueError(f"tensors on different devices ({codes.device} and {x.device})")
+    if codes.dim() != dims:
+        raise ValueError(f"codes of {name} must have {dims} dimensions, got {list(codes.shape)}")
+    rows, k = codes.shape[-2], codes.shape[-1]
+    if k % block:
+        raise ValueError(f"rows of {name} have {k} elements, not a multiple of the block size "
+                         f"{block}")
+    nb = k // block
+    ld = k
+    if not codes.is_contiguous():
+        if dims != 2 or (k > 1 and codes.stride(1) != 1):
+            raise ValueError(f"codes of {name} must have contiguous rows")
+        ld = codes.stride(0) if rows > 1 else k
+    strides = []
+    for x, what in ((alpha, "alpha"), (scale, "scale")):
+        if x.numel() != codes.numel() // block:
+            raise ValueError(f"{what} of {name} must have {codes.numel() // block} elements, got "
+                             f"{x.numel()}")
+        if x.is_contiguous():
+            strides.append(nb)
+        elif dims == 2 and tuple(x.shape) == (rows, nb) and (nb <= 1 or x.stride(1) == 1):
+            strides.append(x.stride(0) if rows > 1 else nb)
+        else:
+            raise ValueError(f"{what} of {name} must be [{rows}, {nb}] with contiguous rows")
+    if strides[0] != strides[1]:
+        raise ValueError(f"alpha and scale of {name} must have the same row stride")
+    return codes.shape, (codes.data_ptr(), ld, alpha.data_ptr(), scale.data_ptr(),
+                         strides[0]), codes.device
+
+
+def _product_out(out, shape, dtype: torch.dtype, device: torch.device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not (isinstance(out, torch.Tensor) and out.is_cuda):
+        raise ValueError("tfp8 operates on GPU tensors only (no CPU path)")
+    if out.device != device:
+        raise ValueError(f"tensors on different devices ({device} and {out.device})")
+    if out.dtype != dtype or tuple(out.shape) != tuple(shape):
+        raise ValueError(f"out must be {dtype} {list(shape)}, got {out.dtype} {list(out.shape)}")
+    return out
+
+
+def _out_rows(out: torch.Tensor) -> int:
+    """Row stride of a 2-D output whose rows are contiguous."""
+    if out.shape[0] and out.shape[1] > 1 and out.stride(1) != 1:
+        raise ValueError("the rows of out must be contiguous")
+    return out.stride(0) if out.shape[0] > 1 else out.shape[1]
+
+
+def compress_t(x: torch.Tensor, block: int = 128, target: float = 1.0, offsets=None, out=None,
+               flags: int = 0):
+    """Compress x^T: x [rows, cols] (bfloat16 or float32, rows at any stride) -> the operand
+    (codes uint8 [cols, kp], alpha, scale float32 [cols, kp / block]) whose blocks run along the
+    rows of x, for products that contract over them.
+
+    offsets (int64 [groups + 1] on the GPU, offsets[0] = 0, ascending) cuts the rows into groups;
+    each group starts at a multiple of the block in the output, kp = padded_rows(rows, groups,
+    block), and what no row fills counts as zeros.  flags: 0 or FLAG_NO_ROTATION."""
+    if not (isinstance(x, torch.Tensor) and x.is_cuda):
+        raise ValueError("tfp8 operates on GPU tensors only (no CPU path)")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [rows, cols], got {list(x.shape)}")
+    if x.dtype == torch.bfloat16:
+        dt = BF16
+    elif x.dtype == torch.float32:
+        dt = F32
+    else:
+        raise ValueError(f"unsupported input dtype {x.dtype}")
+    _product_block(block)
+    rows, cols = x.shape
+    if rows and cols > 1 and x.stride(1) != 1:
+        raise ValueError("the rows of x must be contiguous")
+    ldx = x.stride(0) if rows > 1 else cols
+    groups = 1 if offsets is None else _offsets_of(offsets, x.device)
+    kp = padded_rows(rows, groups, block)
+    if out is None:
+        out = (torch.empty((cols, kp), dtype=torch.uint8, device=x.device),
+               torch.empty((cols, kp // block), dtype=torch.float32, device=x.device),
+               torch.empty((cols, kp // block), dtype=torch.float32, device=x.device))
+    codes, alpha, scale = out
+    _need_gpu(codes, alpha, scale)
+    if codes.device != x.device:
+        raise ValueError(f"tensors on different devices ({x.device} and {codes.device})")
+    _need_buf(codes, torch.uint8, cols * kp, "codes")
+    _need_buf(alpha, torch.float32, cols * (kp // block), "alpha")
+    _need_buf(scale, torch.float32, cols * (kp // block), "scale")
+    with torch.cuda.device(x.device):
+        _check(compress_t_raw(x.data_ptr(), dt, rows, cols, ldx,
+                              None if offsets is None else offsets.data_ptr(), groups, block,
+                              float(target), codes.data_ptr(), alpha.data_ptr(),
+                              scale.data_ptr(), _stream(x), flags))
+    return codes, alpha, scale
+
+
+def matmul(a, b, block: int = 128, dtype: torch.dtype = torch.bfloat16, out=None):
+    """A^ B^T of two compressed operands a = (codes [m, k], alpha, scale) and b = (codes [n, k],
+    alpha, scale), compressed in blocks along k with the same rotation -> [m, n] float32 or
+    bfloat16."""
+    _product_block(block)
+    dt = _out_dtype(dtype)
+    (m, k), ra, dev = _operand(a, block, 2, "a")
+    (n, kb), rb, devb = _operand(b, block, 2, "b")
+    if k != kb:
+        raise ValueError(f"a and b have rows of {k} and {kb} elements")
+    if dev != devb:
+        raise ValueError(f"tensors on different devices ({dev} and {devb})")
+    out = _product_out(out, (m, n), dtype, dev)
+    with torch.cuda.device(dev):
+        _check(matmul_raw(ra, rb, m, n, k, block, out.data_ptr(), dt, _out_rows(out),
+                          _stream(out)))
+    return out
+
+
+def matmul_grouped(a, b, offsets: torch.Tensor, block: int = 128,
+                   dtype: torch.dtype = torch.bfloat16, out=None):
+    """Rows grouped by expert: a = (codes [m, k], ...) with the rows of group g at
+    [offsets[g], offsets[g + 1]), b = (codes [groups, n, k], ...) -> [m, n], each row times its
+    group's b.  Rows past offsets[-1] become zeros."""
+    _product_block(block)
+    dt = _out_dtype(dtype)
+    (m, k), ra, dev = _operand(a, block, 2, "a")
+    (g, n, kb), rb, devb = _operand(b, block, 3, "b")
+    if k != kb:
+        raise ValueError(f"a and b have rows of {k} and {kb} elements")
+    if dev != devb:
+        raise ValueError(f"tensors on different devices ({dev} and {devb})")
+    groups = _offsets_of(offsets, dev)
+    if groups != g:
+        raise ValueError(f"offsets cut {groups} groups and b holds {g}")
+    out = _product_out(out, (m, n), dtype, dev)
+    with torch.cuda.device(dev):
+        _check(matmul_grouped_raw(ra, rb, offsets.data_ptr(), groups, m, n, k, block,
+                                  out.data_ptr(), dt, _out_rows(out), _stream(out)))
+    return out
+
+
+def matmul_grouped_t(a, b, offsets: torch.Tensor, rows: int, block: int = 128,
+                     dtype: torch.dtype = torch.float32, out=None):
+    """Grouped along the contraction: a and b are compress_t's, with the same offsets, of matrices
+    [rows, m] and [rows, n] -> [groups, m, n], for each group the product over its own rows (with
+    a of dY and b of X: each expert's weight gradient).  Zeros for an empty group."""
+    _product_block(block)
+    dt = _out_dtype(dtype)
+    (m, k), ra, dev = _operand(a, block, 2, "a")
+    (n, kb), rb, devb = _operand(b, block, 2, "b")
+    if dev != devb:
+        raise ValueError(f"tensors on different devices ({dev} and {devb})")
+    groups = _offsets_of(offsets, dev)
+    kp = padded_rows(rows, groups, block)
+    if k != kp or kb != kp:
+        raise ValueError(f"{rows} rows in {groups} groups are {kp} elements a row, got {k} and {kb}")
+    out = _product_out(out, (groups, m, n), dtype, dev)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    with torch.cuda.device(dev):
+        _check(matmul_grouped_t_raw(ra, rb, offsets.data_ptr(), groups, rows, m, n, block,
+                                    out.data_ptr(), dt, _stream(out)))
     return out

@@ -4,11 +4,14 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtfp8.so")
-SOURCES = [os.path.join(CSRC, "tfp8_kernels.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in
+           ("tfp8_kernels.hip", "tfp8_compress_t.hip", "tfp8_matmul.hip")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -28,17 +31,27 @@ HIPCC_FLAGS = [
 def build(verbose: bool = False, extra: list[str] | None = None, out: str | None = None) -> str:
     out = out or LIB
     tmp = out + ".tmp"
-    cmd = ["hipcc", *HIPCC_FLAGS, *(extra or []), "-o", tmp, *SOURCES]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    # hipcc's host pass does not know the packed-fp32 feature name; that warning is expected
-    noise = "is not a recognized feature for this target"
-    err = "\n".join(l for l in r.stderr.splitlines() if noise not in l)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({r.returncode}):\n{err}")
-    if verbose and err.strip():
-        print(err, file=sys.stderr)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        # hipcc's host pass does not know the packed-fp32 feature name; that warning is expected
+        noise = "is not a recognized feature for this target"
+        err = "\n".join(l for l in r.stderr.splitlines() if noise not in l)
+        if r.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({r.returncode}):\n{err}")
+        if verbose and err.strip():
+            print(err, file=sys.stderr)
+
+    # one object a source, side by side, then the link
+    flags = [*(f for f in HIPCC_FLAGS if f != "-shared"), *(extra or [])]
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(len(SOURCES)) as pool:
+            list(pool.map(run, (["hipcc", *flags, "-c", "-o", o, s]
+                                for s, o in zip(SOURCES, objects))))
+        run(["hipcc", "--offload-arch=gfx950", "-shared", "-o", tmp, *objects])
     os.replace(tmp, out)
     return out
 

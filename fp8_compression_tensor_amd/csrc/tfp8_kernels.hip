@@ -57,11 +57,9 @@
 #include <math.h>
 #include <stdint.h>
 
-#include <atomic>
-#include <tuple>
-
 #include "../../include/tfp8.h"
 #include "tfp8_device.hpp"
+#include "tfp8_host.hpp"
 
 namespace tfp8 {
 
@@ -1249,20 +1247,6 @@ bool block_ok(int32_t block) {
   return block == 64 || block == 128 || block == 256 || block == 512;
 }
 
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-Range range_of(const void *p, int64_t bytes) {
-  return Range{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-
-bool target_ok(float t) {
-  return isfinite(t) && t >= 0x1p-64f && t <= 0x1p64f;
-}
-
 // Workgroups for a launch with one wavefront per tile, capped at `per_cu` workgroups per
 // compute unit (0: no cap) beyond which the wavefronts loop over tiles.  Measured on MI355X:
 // compress, decompress and the reduce all stream fastest with one tile per wavefront and no loop
@@ -1270,24 +1254,8 @@ bool target_ok(float t) {
 // launch, caps of 2-32 workgroups per CU with prefetching loops were 1-16% slower on
 // 34-940 M-element inputs; over back-to-back launches through rotating buffers the uncapped
 // reduce was 4% faster than at 32 workgroups per CU on the full Qwen-shaped tensor, and equal
-// at one rank's share.
-int cu_count() {
-  // compute units of the current device, looked up once per device (any thread may race to
-  // fill an entry; they all store the same value)
-  constexpr int kMaxDevices = 64;
-  static std::atomic<int> by_device[kMaxDevices];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return 256;
-  int cus = by_device[dev].load(std::memory_order_relaxed);
-  if (cus <= 0) {
-    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-        cus <= 0)
-      cus = 256;
-    by_device[dev].store(cus, std::memory_order_relaxed);
-  }
-  return cus;
-}
-
+// at one rank's share (the caps are TFP8_*_WGS_PER_CU above, 0 in the library).
+//
 // Compress of a large input is 2-4% faster with 64-thread workgroups and each XCD on a
 // contiguous eighth of the tiles: 77% -> 80% of HBM peak for every bf16 input measured from
 // 1.9 to 4.3 GB.  At 1.1 GB the two shapes tie, and on inputs of 134-268 MB the remapped one is
@@ -1305,25 +1273,6 @@ unsigned grid_for(int64_t tiles, int per_cu, int nt = kThreads, bool remap = fal
   int64_t g = wgs < cap ? (wgs > 0 ? wgs : 1) : cap;
   if (remap) g = (g + 7) / 8 * 8;
   return (unsigned)g;
-}
-
-// Launches `kernel` with `args` converted to its parameter types, and returns the status of this
-// launch itself (hipLaunchKernel reports it directly, so an error left over from an earlier,
-// unrelated HIP call is not taken for this launch's).
-template <typename... KArgs, typename... Args>
-tfp8_status launch(void (*kernel)(KArgs...), unsigned grid, int threads, hipStream_t st,
-                   Args... args) {
-  static_assert(sizeof...(KArgs) == sizeof...(Args), "kernel argument count");
-  std::tuple<KArgs...> held(static_cast<KArgs>(args)...);
-  void *argv[sizeof...(KArgs)];
-  std::apply([&argv](auto &...a) {
-    int i = 0;
-    ((argv[i++] = (void *)&a), ...);
-  }, held);
-  return hipLaunchKernel((const void *)kernel, dim3(grid), dim3(threads), argv, 0, st) ==
-                 hipSuccess
-             ? TFP8_OK
-             : TFP8_E_HIP;
 }
 
 template <int B, bool F32, int FLAGS>
@@ -1473,7 +1422,7 @@ tfp8_status launch_accumulate(const uint8_t *codes, const float *alpha, const fl
 
 extern "C" {
 
-int32_t tfp8_version(void) { return (1 << 16) | 3; }
+int32_t tfp8_version(void) { return (1 << 16) | 4; }
 
 const char *tfp8_status_string(tfp8_status status) {
   switch (status) {

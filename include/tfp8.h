@@ -163,6 +163,86 @@ tfp8_status tfp8_accumulate(const uint8_t *codes, const float *alpha, const floa
                             float target, uint32_t flags, uint8_t *codes_out, float *alpha_out,
                             float *scale_out, void *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Products of compressed operands.
+ *
+ * An operand is a matrix compressed in blocks along its rows: codes[rows][k] (row r at codes +
+ * r * ld bytes), alpha and scale[rows][k / block] (row r at alpha + r * lds, scale + r * lds,
+ * floats), as tfp8_compress writes them for a contiguous [rows][k] matrix (ld = k, lds = k /
+ * block), or tfp8_compress_t.  A^ is what the codes stand for (tfp8_decompress).  Both operands of
+ * a product have the same block and the same rotation (both with or both without
+ * TFP8_FLAG_NO_ROTATION): the rotation is orthogonal and leaves a product over whole blocks as it
+ * is, so the kernels multiply the codes and scale the sum of each block,
+ *   C[m][n] = sum over blocks (s_a / alpha_a)(s_b / alpha_b) sum_k dec(qa[m][k]) dec(qb[n][k]),
+ * the sum over blocks in float32.  A block's sum is float32 throughout for float32 outputs.  For
+ * bfloat16 outputs it is the 8-bit matrix instructions', which add eight products of neighbouring
+ * codes at a time with 14 bits from the largest one's down, and the eights in float32: about
+ * 1.4e-5 of the result, a hundredth of the output's own rounding, at twice the rate.  E4M3 codes
+ * only, made by the calls above
+ * (the codes of NaN, 0x7F and 0xFF, do not occur and are outside the contract).  A partial sum
+ * above float32's range gives an infinity or NaN, as it would with the uncompressed operands.
+ *
+ * Common rules: block is 128, 256 or 512 (TFP8_E_BLOCK); rows at most 2^31 - 1, k a multiple of
+ * block and at most 2^22 (TFP8_E_SIZE); ld >= k and lds >= k / block (TFP8_E_ARG), both at most
+ * 2^22 (TFP8_E_SIZE); codes 16-byte aligned, ld a multiple of 16, alpha and scale 4 bytes, out the
+ * size of an element, offsets 8 bytes (TFP8_E_ALIGN).  No output may overlap an input
+ * (TFP8_E_ARG); inputs may overlap one another.  A product with no rows or no columns is a no-op;
+ * with k = 0 it writes zeros.
+ *
+ * Groups.  offsets[groups + 1] (device memory, int64) cuts `rows` rows sorted by group: group g has
+ * rows [offsets[g], offsets[g + 1]), offsets[0] = 0, not descending, offsets[groups] <= rows.  A
+ * group may be empty.  Offsets are clamped to these rules' bounds on the device, so others give
+ * wrong values and no access outside the buffers.  1 <= groups <= TFP8_MAX_GROUPS (TFP8_E_ARG). */
+#define TFP8_MAX_GROUPS 65536
+
+/* Length of a row that holds `rows` rows sorted into `groups` groups, each group rounded up to a
+ * whole block, for any sizes of the groups: block * floor((rows + groups (block - 1)) / block);
+ * with one group, rows rounded up to a block.  0 for arguments out of range. */
+int64_t tfp8_padded_rows(int64_t rows, int32_t groups, int32_t block);
+
+/* Compress of x^T: x[rows][cols] (bfloat16 or float32, row r at x + r * ldx elements, ldx >= cols)
+ * in blocks of `block` rows of one column.  With kp = tfp8_padded_rows(rows, groups, block):
+ * codes[cols][kp], alpha and scale[cols][kp / block], the operand of a product whose contraction
+ * runs over the rows.  Rows past the end of a group's last block count as zeros; blocks past the
+ * last group's are written as zero blocks.  offsets = NULL with groups = 1: all rows are one group.
+ * Rows past offsets[groups] are left out.  flags: 0 or TFP8_FLAG_NO_ROTATION (TFP8_E_ARG: no
+ * product takes INT8 codes).  x is aligned to its elements; any ldx is accepted, and rows that
+ * are aligned to 16 bytes are read faster.  rows * ldx and cols * kp are at most TFP8_MAX_N
+ * (TFP8_E_SIZE). */
+tfp8_status tfp8_compress_t(const void *x, tfp8_dtype x_dtype, int64_t rows, int64_t cols,
+                            int64_t ldx, const int64_t *offsets, int32_t groups, int32_t block,
+                            float target, uint32_t flags, uint8_t *codes, float *alpha,
+                            float *scale, void *stream);
+
+/* out[m][n] (float32, or bfloat16 rounded to nearest even once; row stride ldc >= n elements) =
+ * A^ B^T of the operands A[m][k] and B[n][k]. */
+tfp8_status tfp8_matmul(const uint8_t *a_codes, int64_t a_ld, const float *a_alpha,
+                        const float *a_scale, int64_t a_lds, const uint8_t *b_codes, int64_t b_ld,
+                        const float *b_alpha, const float *b_scale, int64_t b_lds, int64_t m,
+                        int64_t n, int64_t k, int32_t block, void *out, tfp8_dtype out_dtype,
+                        int64_t ldc, void *stream);
+
+/* Grouped by rows: B[groups][n][k] holds one operand per group, one after the other (row r of group
+ * g at row g * n + r; groups * n <= 2^31 - 1), and each row of A[m][k] takes its group's:
+ * out[r] = A^[r] B^[g(r)]^T.  Rows past offsets[groups] become zeros. */
+tfp8_status tfp8_matmul_grouped(const uint8_t *a_codes, int64_t a_ld, const float *a_alpha,
+                                const float *a_scale, int64_t a_lds, const uint8_t *b_codes,
+                                int64_t b_ld, const float *b_alpha, const float *b_scale,
+                                int64_t b_lds, const int64_t *offsets, int32_t groups, int64_t m,
+                                int64_t n, int64_t k, int32_t block, void *out,
+                                tfp8_dtype out_dtype, int64_t ldc, void *stream);
+
+/* Grouped along the contraction: A[m][kp] and B[n][kp] are tfp8_compress_t's of matrices with
+ * `rows` rows cut by the same offsets, and out[groups][m][n] (contiguous) gets, for each group, the
+ * product over that group's rows alone: a weight gradient per expert.  Zeros for an empty group.
+ * kp = tfp8_padded_rows(rows, groups, block). */
+tfp8_status tfp8_matmul_grouped_t(const uint8_t *a_codes, int64_t a_ld, const float *a_alpha,
+                                  const float *a_scale, int64_t a_lds, const uint8_t *b_codes,
+                                  int64_t b_ld, const float *b_alpha, const float *b_scale,
+                                  int64_t b_lds, const int64_t *offsets, int32_t groups,
+                                  int64_t rows, int64_t m, int64_t n, int32_t block, void *out,
+                                  tfp8_dtype out_dtype, void *stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *tfp8_status_string(tfp8_status status);
 
