@@ -20,7 +20,9 @@ namespace tfp8 {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void lds_void;
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef const __attribute__((address_space(3))) void lds_const;
 
 constexpr int kStep = 128;  // contraction depth of one matrix instruction
 
@@ -93,16 +95,54 @@ __device__ __forceinline__ Fragment<WIDE> make_fragment(u32x4 lo, u32x4 hi) {
   return f;
 }
 
+// part[j] = x[j] y for all j: the wide form goes over the quarters outermost, so that neighbouring
+// instructions do not wait for one another.
+template <int N>
+__device__ __forceinline__ void mfma_row(f32x4 (&part)[N], const Fragment<true> (&x)[N],
+                                         const Fragment<true> &y) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+      part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j].v[t], y.v[t], t ? part[j] : zero, 0, 0,
+                                                        0);
+    }
+}
 __device__ __forceinline__ f32x4 mfma_codes(const Fragment<false> &x, const Fragment<false> &y) {
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.v, y.v, zero, 0, 0, 0, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4 mfma_codes(const Fragment<true> &x, const Fragment<true> &y) {
-  f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.v[t], y.v[t], d, 0, 0, 0);
-  return d;
+
+// A raw buffer descriptor: reads at or past `bytes` give zeros.
+__device__ __forceinline__ i32x4 buffer_of(const void *base, int64_t bytes) {
+  const uint64_t p = (uint64_t)base;
+  return i32x4{__builtin_amdgcn_readfirstlane((int)p),
+               __builtin_amdgcn_readfirstlane((int)(p >> 32) & 0xFFFF),
+               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+
+// 16 bytes a lane from the buffer at offset voff + soff to LDS, lane l's at to + 16 l.  Written as
+// asm because the compiler waits for every such load in flight before any read of LDS, also of
+// the other stage; it returns no register, and the caller waits for it with wait_loads().  m0, which
+// holds the address, has no other use in these kernels.
+__device__ __forceinline__ void load_to_lds(i32x4 buffer, int voff, int soff, const void *to) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_const *)to);
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(at), "v"(voff), "s"(buffer), "s"(soff)
+      : "memory");
+}
+// Every load of this wavefront, to registers or to LDS, has arrived.
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Every LDS access of this wavefront is done, then those of the whole workgroup.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 template <bool F32OUT>
@@ -137,30 +177,32 @@ __device__ __forceinline__ void store_values(void *out, int64_t at, const f32x4 
   }
 }
 
-template <int BM, int BN, int WM, int WN, int MODE, bool F32OUT>
-__device__ __forceinline__ void matmul_tile(const ProductArgs &p) {
-  constexpr int NW = WM * WN;
-  constexpr int TM = BM / 16 / WM, TN = BN / 16 / WN;
-  constexpr int ROWS = BM + BN;
-  constexpr int NT = 64 * NW;
-  constexpr int LOADS = ROWS / 8 / NW;  // 1 KB loads of a wavefront a step (8 rows each)
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole loads of one operand");
-  constexpr int SC = (ROWS + NT - 1) / NT;  // rows whose scales a thread prepares
-  __shared__ alignas(1024) uint8_t tile[2][ROWS * kStep];
-  __shared__ float rsc[2][ROWS];
+// What a workgroup computes: rows [m0, m0 + mv) of A by rows [n0, n0 + nv) of B over the steps
+// [s0, s1), and where it goes.
+struct Job {
+  const uint8_t *ac, *bc;          // codes of the first rows
+  const float *aa, *as, *ba, *bs;  // their scales
+  char *out;                       // the first element
+  int mv, nv;
+  int s0, s1;
+};
 
-  const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int q = lane >> 4, l16 = lane & 15;
-  const int wm = w / WN, wn = w % WN;
+// The workgroup's tile.  Neighbouring workgroups go to different XCDs, each with an L2 of its own,
+// so tiles are dealt out in eight contiguous parts, and run down bands of kBand tiles of A: what an
+// XCD works on at one time then shares rows on both sides.  (8192 x 8192 x 8192: 595 us, against
+// 677 in the same bands without the parts; one band of 16, 618.)  The parts of a product over
+// ragged depths would be uneven (561 us against 454), and stay in plain order.
+constexpr int kBand = 4;
 
-  // the tile of this workgroup
+template <int BM, int BN, int MODE, int ES>
+__device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
   int64_t bid = blockIdx.x;
-  int64_t m0, m1, n0, s0 = 0, s1 = p.steps;
-  Operand a = p.a, b = p.b;
+  if constexpr (MODE != kGroupedDepth) {
+    const unsigned per = gridDim.x >> 3, over = gridDim.x & 7, x = blockIdx.x & 7;
+    bid = x * per + (x < over ? x : over) + (blockIdx.x >> 3);
+  }
   char *out = (char *)p.out;
-  constexpr int ES = F32OUT ? 4 : 2;
+  int64_t s0 = 0, s1 = p.steps;
   if constexpr (MODE == kGroupedDepth) {
     const int per = p.mtiles * p.ntiles;
     const int e = (int)(bid / per);
@@ -172,147 +214,437 @@ __device__ __forceinline__ void matmul_tile(const ProductArgs &p) {
     s0 = s0 < s1 ? s0 : s1;
     out += (int64_t)e * p.next_c * ES;
   }
-  const int mt = (int)(bid / p.ntiles), nt = (int)(bid % p.ntiles);
-  n0 = (int64_t)nt * BN;
+  const int band = kBand * p.ntiles;
+  const int b0 = (int)(bid / band) * kBand, in_band = (int)(bid % band);
+  const int high = p.mtiles - b0 < kBand ? p.mtiles - b0 : kBand;
+  const int mt = b0 + in_band % high, nt = in_band / high;
+  const int64_t n0 = (int64_t)nt * BN;
+  int64_t m0, bskip = 0, bskip_s = 0;
   if constexpr (MODE == kGroupedRows) {
     const GroupTile g = tile_of_groups(p.offsets, p.groups, p.m, BM, mt, p.groups);
-    if (g.rows <= 0) return;
+    if (g.rows <= 0) return false;
     m0 = g.row0;
-    m1 = g.row0 + g.rows;
+    t.mv = g.rows;
     if (g.group == p.groups) {  // rows past the last group: zeros
       s1 = 0;
     } else {
-      b.codes += (int64_t)g.group * b.next;
-      b.alpha += (int64_t)g.group * b.next_s;
-      b.scale += (int64_t)g.group * b.next_s;
+      bskip = (int64_t)g.group * p.b.next;
+      bskip_s = (int64_t)g.group * p.b.next_s;
     }
   } else {
     m0 = (int64_t)mt * BM;
-    m1 = m0 + BM < p.m ? m0 + BM : p.m;
+    t.mv = (int)(p.m - m0 < BM ? p.m - m0 : BM);
   }
-  const int mv = (int)(m1 - m0);
-  const int nv = (int)(n0 + BN < p.n ? BN : p.n - n0);
+  t.nv = (int)(p.n - n0 < BN ? p.n - n0 : BN);
+  t.s0 = (int)s0;
+  t.s1 = (int)s1;
+  t.ac = p.a.codes + m0 * p.a.ld;
+  t.aa = p.a.alpha + m0 * p.a.lds;
+  t.as = p.a.scale + m0 * p.a.lds;
+  t.bc = p.b.codes + bskip + n0 * p.b.ld;
+  t.ba = p.b.alpha + bskip_s + n0 * p.b.lds;
+  t.bs = p.b.scale + bskip_s + n0 * p.b.lds;
+  t.out = out + (m0 * p.ldc + n0) * ES;
+  return true;
+}
 
-  // Loads.  A wavefront's load instruction fills 8 rows of 128 bytes of LDS, lane i the i-th 16
-  // bytes; it takes them from chunk (i & 7) ^ (row & 7) of its row, so that the lanes that read
-  // a column of fragments touch all banks.  Rows past the operand's end read as zeros (the
-  // descriptor's bound).
-  const auto ra = __builtin_amdgcn_make_buffer_rsrc(
-      (void *)(a.codes + m0 * a.ld), 0, (int)((mv - 1) * a.ld + p.steps * kStep), 0x00020000);
-  const auto rb = __builtin_amdgcn_make_buffer_rsrc(
-      (void *)(b.codes + n0 * b.ld), 0, (int)((nv - 1) * b.ld + p.steps * kStep), 0x00020000);
-  int voff[LOADS];
+// LDS of a tile: two stages of a step's codes, A's rows then B's, and their scales r.
+template <int BM, int BN>
+struct Stages {
+  alignas(1024) uint8_t codes[2][(BM + BN) * kStep];
+  float r[2][BM + BN];
+};
+
+// Filling the stages.
+template <int BM, int BN, int NW>
+struct Feed {
+  static constexpr int ROWS = BM + BN, NT = 64 * NW;
+  static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // a wavefront's loads a step
+  static constexpr int SC = (ROWS + NT - 1) / NT;           // rows whose scales a thread prepares
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole loads of one operand");
+  static_assert(BM % 64 == 0 && ROWS % 64 == 0, "a wavefront's scales are of one operand");
+
+  Stages<BM, BN> &lds;
+  int w, shift, first, blocks;
+  i32x4 ra[LA], rb[LB];
+  int va, vb;
+  const char *sp[SC], *ap[SC];  // a wavefront's rows are of one operand
+  uint32_t at0[SC];
+  f32x4 sv[SC], av[SC];
+
+  // A wavefront's load instruction fills 8 rows of 128 bytes of LDS, lane i the i-th 16 bytes; it
+  // takes them from chunk (i & 7) ^ (row & 7) of its row, so that the lanes that read a column of
+  // fragments touch all banks.  Each instruction has a descriptor of its own, from its first row on
+  // to the operand's end, past which rows read as zeros.
+  __device__ __forceinline__ Feed(Stages<BM, BN> &l, const ProductArgs &p, const Job &t)
+      : lds(l), shift(p.shift) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+    va = (lane >> 3) * (int)p.a.ld + chunk;
+    vb = (lane >> 3) * (int)p.b.ld + chunk;
+    const int64_t k = p.steps * kStep;
 #pragma unroll
-  for (int i = 0; i < LOADS; ++i) {
-    const int row = (i * NW + w) * 8 + (lane >> 3);
-    const int chunk = (lane & 7) ^ (row & 7);
-    voff[i] = row < BM ? row * (int)a.ld + chunk * 16 : (row - BM) * (int)b.ld + chunk * 16;
-  }
-  auto load_step = [&](int64_t s, int stage) {
-    const int k0 = (int)(s * kStep);
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      lds_void *to = (lds_void *)&tile[stage][(i * NW + w) * 1024];
-      if (i < BM / 8 / NW)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to, 16, voff[i], k0, 0, 0);
-      else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, to, 16, voff[i], k0, 0, 0);
+    for (int i = 0; i < LA; ++i) {
+      const int row = (i * NW + w) * 8;
+      const int64_t left = (int64_t)(t.mv - 1 - row) * p.a.ld + k;
+      ra[i] = buffer_of(t.ac + (int64_t)row * p.a.ld, left > 0 ? left : 0);
     }
-  };
-  // scales: thread t prepares r = scale / alpha of row t (A's rows, then B's)
-  const float *sp[SC], *ap[SC];
 #pragma unroll
-  for (int i = 0; i < SC; ++i) {
-    int row = tid + i * NT;
-    row = row < ROWS ? row : ROWS - 1;
-    const bool isa = row < BM;
-    int64_t rr = isa ? row : row - BM;
-    const int64_t last = (isa ? mv : nv) - 1;
-    rr = rr < last ? rr : last;
-    const int64_t at = isa ? (m0 + rr) * a.lds : (n0 + rr) * b.lds;
-    sp[i] = (isa ? a.scale : b.scale) + at;
-    ap[i] = (isa ? a.alpha : b.alpha) + at;
-  }
-  float sv[SC], av[SC];
-  auto load_scales = [&](int64_t s) {
+    for (int i = 0; i < LB; ++i) {
+      const int row = (i * NW + w) * 8;
+      const int64_t left = (int64_t)(t.nv - 1 - row) * p.b.ld + k;
+      rb[i] = buffer_of(t.bc + (int64_t)row * p.b.ld, left > 0 ? left : 0);
+    }
 #pragma unroll
     for (int i = 0; i < SC; ++i) {
-      sv[i] = sp[i][s >> p.shift];
-      av[i] = ap[i][s >> p.shift];
+      const bool isa = w * 64 + i * NT < BM;
+      int rr = tid + i * NT - (isa ? 0 : BM);
+      const int last = (isa ? t.mv : t.nv) - 1;
+      rr = rr < last ? rr : last;
+      at0[i] = (uint32_t)(rr * (int)(isa ? p.a.lds : p.b.lds)) * 4;  // below 2^30
+      sp[i] = (const char *)(isa ? t.as : t.bs);
+      ap[i] = (const char *)(isa ? t.aa : t.ba);
     }
-  };
-  auto put_scales = [&](int stage) {
-#pragma unroll
-    for (int i = 0; i < SC; ++i)
-      if (tid + i * NT < ROWS) rsc[stage][tid + i * NT] = __fdiv_rn(sv[i], av[i]);
-  };
+    first = t.s0 >> shift;
+    blocks = (int)(p.steps >> shift);
+  }
 
+  // The part-th of `parts` shares of a step's loads.
+  __device__ __forceinline__ void load_step(int s, int stage, int part = 0, int parts = 1) {
+#pragma unroll
+    for (int i = 0; i < LA + LB; ++i) {
+      if (i * parts / (LA + LB) != part) continue;
+      if (i < LA)
+        load_to_lds(ra[i], va, s * kStep, &lds.codes[stage][(i * NW + w) * 1024]);
+      else
+        load_to_lds(rb[i - LA], vb, s * kStep,
+                    &lds.codes[stage][BM * kStep + ((i - LA) * NW + w) * 1024]);
+    }
+  }
+  // Scales: thread t prepares r = scale / alpha of row t (A's rows, then B's).  They lie a row
+  // apart in memory, a cache line each, so four blocks' are loaded at once: called for every
+  // step, this loads at the first of four blocks.
+  __device__ __forceinline__ void load_scales(int s) {
+    const int at = s >> shift;
+    if (((at - first) & 3) || (s & ((1 << shift) - 1))) return;
+#pragma unroll
+    for (int i = 0; i < SC; ++i) {
+      const char *ss = sp[i] + at * 4, *aa = ap[i] + at * 4;
+      if (at + 4 <= blocks) {
+        sv[i] = *(const f32x4u *)(ss + at0[i]);
+        av[i] = *(const f32x4u *)(aa + at0[i]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          sv[i][k] = at + k < blocks ? *(const float *)(ss + at0[i] + 4 * k) : 0.0f;
+          av[i][k] = at + k < blocks ? *(const float *)(aa + at0[i] + 4 * k) : 1.0f;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void put_scales(int s, int stage) {
+    const int k = ((s >> shift) - first) & 3;
+#pragma unroll
+    for (int i = 0; i < SC; ++i) {
+      const float x = k & 2 ? (k & 1 ? sv[i][3] : sv[i][2]) : (k & 1 ? sv[i][1] : sv[i][0]);
+      const float y = k & 2 ? (k & 1 ? av[i][3] : av[i][2]) : (k & 1 ? av[i][1] : av[i][0]);
+      const int row = (int)threadIdx.x + i * NT;
+      if (ROWS % NT == 0 || row < ROWS) lds.r[stage][row] = x * __builtin_amdgcn_rcpf(y);
+    }
+  }
+};
+
+// Lane l takes chunks q and q + 4 of row l & 15 of a 16-row tile; `at` is fragment_offset of the
+// tile's first row.  With these chunks a read takes 4 cycles, all banks busy (measured; 2 q and
+// 2 q + 1, which look as good, meet in pairs and take 8).
+__device__ __forceinline__ int fragment_offset(int row, int q, int l16) {
+  return (row + l16) * kStep + ((q ^ (l16 & 7)) << 4);
+}
+template <bool WIDE>
+__device__ __forceinline__ Fragment<WIDE> read_fragment(const uint8_t *codes, int at) {
+  return make_fragment<WIDE>(*(const u32x4 *)(codes + at), *(const u32x4 *)(codes + (at ^ 64)));
+}
+
+// The loop over steps, for wavefronts of TM x TN tiles.  The scaled addition of a tile's partial
+// products follows TN matrix instructions behind the one that makes them, so that neither waits for
+// the other.  One barrier a step, before the last row of tiles: by then the step's fragments are in
+// registers, so the loads of the step after next may overwrite them, and the next step's first
+// fragments are read under the last row's products.
+template <int BM, int BN, int TM, int TN, bool WIDE, class FEED>
+__device__ __forceinline__ void run_steps(Stages<BM, BN> &lds, FEED &feed, int s0, int s1,
+                                          int mrow, int nrow, f32x4 (&acc)[TM][TN]) {
+  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+  const int fa0 = fragment_offset(mrow, q, l16), fb0 = fragment_offset(BM + nrow, q, l16);
+  constexpr int NP = TM >= 8 ? 3 : 2;  // a step's loads go out in this many shares
+  int s = s0;
+  feed.load_step(s, 0);
+  feed.load_scales(s);
+  wait_loads();
+  feed.put_scales(s, 0);
+  lds_barrier();
+  if (s + 1 < s1) {
+    feed.load_step(s + 1, 1, 0, NP);
+    if (NP == 1) feed.load_scales(s + 1);
+  }
+  Fragment<WIDE> fb[TN], fa;
+  f32x4 rb[TN], part[TN];
+  float ra, rprev = 0.0f;  // A's scales of this row of tiles and of the one before
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    fb[j] = read_fragment<WIDE>(lds.codes[0], fb0 + j * 16 * kStep);
+    rb[j] = part[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  fa = read_fragment<WIDE>(lds.codes[0], fa0);
+  ra = lds.r[0][mrow + l16];
+  // part[j] of the row of tiles before, scaled and added
+  auto add_part = [&](f32x4 (&to)[TN], int j) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) to[j][k] = fmaf(part[j][k], rprev * rb[j][k], to[j][k]);
+    // keeps the addition here: the compiler would move it past the branches below, and keep
+    // every partial product until then
+    asm volatile("" : "+v"(to[j]));
+  };
+  for (int stage = 0; s < s1; ++s, stage ^= 1) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const bool last = i == TM - 1;
+      if (last) {
+        wait_loads();
+        if (s + 1 < s1) feed.put_scales(s + 1, stage ^ 1);
+        lds_barrier();
+        if (s + 2 < s1) {
+          feed.load_step(s + 2, stage, 0, NP);
+          if (NP == 1) feed.load_scales(s + 2);
+        }
+      } else if (i + 1 < NP && s + 1 < s1) {
+        feed.load_step(s + 1, stage ^ 1, i + 1, NP);
+        if (i + 2 == NP) feed.load_scales(s + 1);
+      }
+      const int ns = last ? stage ^ 1 : stage;
+      const int ni = last ? 0 : i + 1;
+      const Fragment<WIDE> fn = read_fragment<WIDE>(lds.codes[ns], fa0 + ni * 16 * kStep);
+      const float rn = lds.r[ns][mrow + ni * 16 + l16];
+      // B's scales of this step replace the last one's once its last row is added
+      auto next_scales = [&](int j) {
+        if (i == 0) rb[j] = *(const f32x4 *)&lds.r[stage][BM + nrow + j * 16 + 4 * q];
+      };
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          add_part(acc[i ? i - 1 : TM - 1], j);
+          next_scales(j);
+        }
+        mfma_row(part, fb, fa);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          if (last) fb[j] = read_fragment<WIDE>(lds.codes[ns], fb0 + j * 16 * kStep);
+      } else {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          add_part(acc[i ? i - 1 : TM - 1], j);
+          next_scales(j);
+          part[j] = mfma_codes(fb[j], fa);
+          if (last) fb[j] = read_fragment<WIDE>(lds.codes[ns], fb0 + j * 16 * kStep);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      fa = fn;
+      rprev = ra;
+      ra = rn;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < TN; ++j) add_part(acc[TM - 1], j);
+}
+
+// The kernel only calls this function: a kernel's own body is also read by the host's pass, which
+// does not know these builtins.
+template <int BM, int BN, int WM, int WN, int MODE, bool F32OUT>
+__device__ __forceinline__ void matmul_tile(const ProductArgs &p) {
+  constexpr int TM = BM / 16 / WM, TN = BN / 16 / WN;
+  __shared__ Stages<BM, BN> lds;
+  Job t;
+  if (!find_job<BM, BN, MODE, F32OUT ? 4 : 2>(p, t)) return;
+  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int mrow = w / WN * TM * 16, nrow = w % WN * TN * 16;
   f32x4 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  if (s0 < s1) {
-    load_step(s0, 0);
-    load_scales(s0);
+  if (t.s0 < t.s1) {
+    Feed<BM, BN, WM * WN> feed(lds, p, t);
+    run_steps<BM, BN, TM, TN, F32OUT>(lds, feed, t.s0, t.s1, mrow, nrow, acc);
   }
-  for (int64_t s = s0; s < s1; ++s) {
-    const int stage = (int)(s - s0) & 1;
-    put_scales(stage);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (s + 1 < s1) {
-      load_step(s + 1, stage ^ 1);
-      load_scales(s + 1);
-    }
-    const uint8_t *tl = tile[stage];
-    auto fragment = [&](int row) {
-      const int at = row * kStep + (((2 * q) ^ (row & 7)) << 4);
-      return make_fragment<F32OUT>(*(const u32x4 *)(tl + at), *(const u32x4 *)(tl + (at ^ 16)));
-    };
-    Fragment<F32OUT> fb[TN];
-    f32x4 rbv[TN];
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int row = BM + (wn * TN + j) * 16;
-      fb[j] = fragment(row + l16);
-      rbv[j] = *(const f32x4 *)&rsc[stage][row + 4 * q];
-    }
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int row = (wm * TM + i) * 16 + l16;
-      const Fragment<F32OUT> fa = fragment(row);
-      const float rav = rsc[stage][row];
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const f32x4 part = mfma_codes(fb[j], fa);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(part[k], rav * rbv[j][k], acc[i][j][k]);
-      }
-    }
-  }
-
-  const bool wide = ((uintptr_t)out % (4 * ES) == 0) && (p.ldc % 4 == 0);
+  const bool wide = ((uintptr_t)t.out % (F32OUT ? 16 : 8) == 0) && (p.ldc % 4 == 0);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int row = (wm * TM + i) * 16 + l16;
-    if (row < mv) {
+    const int row = mrow + i * 16 + l16;
+    if (row < t.mv) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        const int col = (wn * TN + j) * 16 + 4 * q;
-        store_values<F32OUT>(out, (m0 + row) * p.ldc + n0 + col, acc[i][j], nv - col, wide);
+        const int col = nrow + j * 16 + 4 * q;
+        store_values<F32OUT>(t.out, row * p.ldc + col, acc[i][j], t.nv - col, wide);
       }
     }
   }
 }
 
-// The kernel only calls the function above: the host's pass over a kernel's own body does not know
-// the buffer descriptors' type.
 template <int BM, int BN, int WM, int WN, int MODE, bool F32OUT>
-__global__ __launch_bounds__(64 * WM * WN) void k_matmul_tile(ProductArgs p) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_matmul_tile(ProductArgs p) {
   matmul_tile<BM, BN, WM, WN, MODE, F32OUT>(p);
+}
+
+// --------------------------------------------------------------------------------------------
+// Few rows (decoding): the product reads B once and is bound by that, so it keeps as many of its
+// bytes in flight as it can and shares nothing.  A workgroup takes 16 MT rows of A (its group's) and
+// 16 TN of B; its eight wavefronts take turns at chunks of four steps, reading the fragments straight
+// from memory into registers (lane l: chunks q and q + 4 of row l & 15, so that an instruction's four
+// lanes of a row take 64 bytes of it), and add up through LDS in a fixed order at the end.  A's
+// scales are prepared in LDS for the whole depth first, B's are read four blocks at a time.  Products
+// are of rows of A by rows of B here: D[4 q + i][l & 15] is row m = 4 q + i and column n = l & 15, so
+// that a lane needs one scale of B.
+constexpr int kFewWaves = 8, kFewChunk = 4;
+constexpr int kFewScales = 8192;  // scales of A that fit: rows of a workgroup times blocks of a row
+
+template <bool WIDE>
+__device__ __forceinline__ Fragment<WIDE> load_fragment(const uint8_t *row, int q) {
+  return make_fragment<WIDE>(*(const u32x4 *)(row + q * 16), *(const u32x4 *)(row + q * 16 + 64));
+}
+__device__ __forceinline__ f32x4 mfma_one(const Fragment<false> &x, const Fragment<false> &y) {
+  return mfma_codes(x, y);
+}
+__device__ __forceinline__ f32x4 mfma_one(const Fragment<true> &x, const Fragment<true> &y) {
+  f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.v[t], y.v[t], d, 0, 0, 0);
+  return d;
+}
+
+template <int MT, int TN, int MODE, bool F32OUT>
+__device__ __forceinline__ void matmul_few(const ProductArgs &p) {
+  constexpr int BM = 16 * MT, BN = 16 * TN;
+  __shared__ union {
+    float r[kFewScales];                          // A's scales, [row][block]
+    float sum[kFewWaves][MT * TN][16][17];        // the wavefronts' sums
+  } lds;
+  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, l16 = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int mt = (int)(blockIdx.x % p.mtiles), nt = (int)(blockIdx.x / p.mtiles);
+  const int64_t n0 = (int64_t)nt * BN;
+  int64_t m0 = (int64_t)mt * BM, bskip = 0, bskip_s = 0;
+  int mv, steps = (int)p.steps;
+  if constexpr (MODE == kGroupedRows) {
+    const GroupTile g = tile_of_groups(p.offsets, p.groups, p.m, BM, mt, p.groups);
+    if (g.rows <= 0) return;
+    m0 = g.row0;
+    mv = g.rows;
+    if (g.group == p.groups) {  // rows past the last group: zeros
+      steps = 0;
+    } else {
+      bskip = (int64_t)g.group * p.b.next;
+      bskip_s = (int64_t)g.group * p.b.next_s;
+    }
+  } else {
+    mv = (int)(p.m - m0 < BM ? p.m - m0 : BM);
+  }
+  const int nv = (int)(p.n - n0 < BN ? p.n - n0 : BN);
+  const int blocks = steps >> p.shift;
+
+  // the rows of this lane's fragments; past the end, the last row again
+  const uint8_t *ar[MT], *br[TN];
+  const float *ba[TN], *bs[TN];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int row = i * 16 + l16 < mv ? i * 16 + l16 : mv - 1;
+    ar[i] = p.a.codes + (m0 + row) * p.a.ld;
+  }
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int row = j * 16 + l16 < nv ? j * 16 + l16 : nv - 1;
+    br[j] = p.b.codes + bskip + (n0 + row) * p.b.ld;
+    ba[j] = p.b.alpha + bskip_s + (n0 + row) * p.b.lds;
+    bs[j] = p.b.scale + bskip_s + (n0 + row) * p.b.lds;
+  }
+  for (int at = tid; at < BM * blocks; at += 64 * kFewWaves) {
+    const int row = at / blocks, b = at - row * blocks;
+    const int64_t from = (m0 + (row < mv ? row : mv - 1)) * p.a.lds + b;
+    lds.r[at] = p.a.scale[from] * __builtin_amdgcn_rcpf(p.a.alpha[from]);
+  }
+  __syncthreads();
+
+  f32x4 acc[MT][TN];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = w * kFewChunk; s < steps; s += kFewWaves * kFewChunk) {
+    Fragment<F32OUT> fa[kFewChunk][MT], fb[kFewChunk][TN];
+    float rb[kFewChunk][TN];
+#pragma unroll
+    for (int u = 0; u < kFewChunk; ++u) {
+      const int su = s + u < steps ? s + u : steps - 1;  // past the end: read again, left out below
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        fb[u][j] = load_fragment<F32OUT>(br[j] + (int64_t)su * kStep, q);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int b = su >> p.shift;
+        rb[u][j] = bs[j][b] * __builtin_amdgcn_rcpf(ba[j][b]);
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        fa[u][i] = load_fragment<F32OUT>(ar[i] + (int64_t)su * kStep, q);
+    }
+#pragma unroll
+    for (int u = 0; u < kFewChunk; ++u) {
+      if (s + u < steps) {
+        const int b = (s + u) >> p.shift;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          float ra[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ra[k] = lds.r[(i * 16 + 4 * q + k) * blocks + b];
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            const f32x4 part = mfma_one(fa[u][i], fb[u][j]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              acc[i][j][k] = fmaf(part[k], ra[k] * rb[u][j], acc[i][j][k]);
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) lds.sum[w][i * TN + j][4 * q + k][l16] = acc[i][j][k];
+  __syncthreads();
+  for (int at = tid; at < BM * BN; at += 64 * kFewWaves) {
+    const int m = at / BN, n = at % BN;
+    if (m < mv && n < nv) {
+      float v = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kFewWaves; ++k) v += lds.sum[k][m / 16 * TN + n / 16][m % 16][n % 16];
+      const int64_t to = (m0 + m) * p.ldc + n0 + n;
+      if constexpr (F32OUT)
+        ((float *)p.out)[to] = v;
+      else
+        ((__bf16 *)p.out)[to] = (__bf16)v;
+    }
+  }
+}
+
+template <int MT, int TN, int MODE, bool F32OUT>
+__global__ __launch_bounds__(64 * kFewWaves) void k_matmul_few(ProductArgs p) {
+  matmul_few<MT, TN, MODE, F32OUT>(p);
 }
 
 }  // namespace tfp8
@@ -323,18 +655,51 @@ using namespace tfp8;
 
 bool product_block_ok(int32_t block) { return block == 128 || block == 256 || block == 512; }
 
-template <int MODE, bool F32OUT>
-tfp8_status launch_product(ProductArgs p, hipStream_t st) {
-  constexpr int BM = 128, BN = 128;
-  int64_t mt = (p.m + BM - 1) / BM;
-  if (MODE == kGroupedRows) mt = (p.m + (int64_t)(p.groups + 1) * (BM - 1)) / BM;
-  const int64_t nt = (p.n + BN - 1) / BN;
-  int64_t grid = mt * nt;
-  if (MODE == kGroupedDepth) grid *= p.groups;
-  if (grid > (((int64_t)1 << 32) - 1) / 256) return TFP8_E_SIZE;
+// Launches `kernel` with one workgroup for each of mt x nt tiles (times `times`).
+tfp8_status launch_tiles(void (*kernel)(ProductArgs), ProductArgs p, int bm, int bn, int64_t times,
+                         int threads, hipStream_t st) {
+  // tiles that groups of any sizes can come to, with the rows past the last as one more group
+  const int64_t mt = p.offsets && p.next_c == 0
+                         ? (p.m + (int64_t)(p.groups + 1) * (bm - 1)) / bm
+                         : (p.m + bm - 1) / bm;
+  const int64_t nt = (p.n + bn - 1) / bn;
+  if (mt * nt > (((int64_t)1 << 32) - 1) / threads / times) return TFP8_E_SIZE;
   p.mtiles = (int)mt;
   p.ntiles = (int)nt;
-  return launch(k_matmul_tile<BM, BN, 2, 2, MODE, F32OUT>, (unsigned)grid, 256, st, p);
+  return launch(kernel, (unsigned)(mt * nt * times), threads, st, p);
+}
+
+template <int MODE, bool F32OUT>
+tfp8_status launch_product(const ProductArgs &p, hipStream_t st) {
+  const int64_t times = MODE == kGroupedDepth ? p.groups : 1;
+  // rows that share a B: all of them, or an even share of them a group
+  const int64_t together = MODE == kGroupedRows ? (p.m + p.groups - 1) / p.groups : p.m;
+  if constexpr (MODE != kGroupedDepth) {
+    const int64_t blocks = p.steps >> p.shift;
+    if (together <= 16 && 16 * blocks <= kFewScales)
+      return launch_tiles(k_matmul_few<1, 1, MODE, F32OUT>, p, 16, 16, 1, 64 * kFewWaves, st);
+    if (together <= 32 && 32 * blocks <= kFewScales)
+      return launch_tiles(k_matmul_few<2, 2, MODE, F32OUT>, p, 32, 32, 1, 64 * kFewWaves, st);
+  }
+  // Large tiles, one workgroup a compute unit, or small ones, two a unit: slower for the same work,
+  // but with less left over at the edges and in the last round.  Whichever is done sooner, by the
+  // nanoseconds a step of a round took (8192 x 8192 x 8192): 2150 for 256 x 256 and 1470 for 128 x
+  // 128 with bfloat16 outputs, 2050 for 256 x 128 and 2140 with float32 ones; a last round of small
+  // tiles that leaves every unit one at most takes 0.6 of that.
+  const int64_t cus = cu_count();
+  const auto tiles = [&](int bm, int bn) {
+    int64_t mt = (p.m + bm - 1) / bm;
+    if (MODE == kGroupedRows) mt += p.groups / 2;  // half a tile a group is left over
+    return mt * ((p.n + bn - 1) / bn) * times;
+  };
+  constexpr int BM = 256, BN = F32OUT ? 128 : 256;
+  const int64_t large = (tiles(BM, BN) + cus - 1) / cus * (F32OUT ? 2050 : 2150);
+  const int64_t small = tiles(128, 128), rest = small % (2 * cus), t = F32OUT ? 2140 : 1470;
+  const int64_t small_ns = small / (2 * cus) * t + (rest > cus ? t : rest ? t * 6 / 10 : 0);
+  if (large < small_ns)
+    return launch_tiles(k_matmul_tile<BM, BN, F32OUT ? 4 : 2, F32OUT ? 2 : 4, MODE, F32OUT>, p, BM,
+                        BN, times, 512, st);
+  return launch_tiles(k_matmul_tile<128, 128, 2, 2, MODE, F32OUT>, p, 128, 128, times, 256, st);
 }
 
 template <int MODE>
@@ -344,11 +709,12 @@ tfp8_status launch_product(const ProductArgs &p, bool f32, hipStream_t st) {
 
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;  // rows and columns of one operand
 constexpr int64_t kMaxLd = (int64_t)1 << 22;          // codes of a row: a tile's offsets fit 31 bits
+constexpr int64_t kMaxLds = (int64_t)1 << 20;         // scales of a row
 
 // Checks of one operand [rows, k] (count of them, `next` bytes apart): strides, pointers.
 tfp8_status operand_sizes(int64_t rows, int64_t k, int32_t block, int64_t ld, int64_t lds) {
   if (rows < 0 || rows > kMaxRows || k < 0 || k > kMaxLd || k % block != 0) return TFP8_E_SIZE;
-  if (ld > kMaxLd || lds > kMaxLd) return TFP8_E_SIZE;
+  if (ld > kMaxLd || lds > kMaxLds) return TFP8_E_SIZE;
   if (ld < k || lds < k / block) return TFP8_E_ARG;
   return TFP8_OK;
 }

@@ -183,8 +183,8 @@ tfp8_status tfp8_accumulate(const uint8_t *codes, const float *alpha, const floa
  * above float32's range gives an infinity or NaN, as it would with the uncompressed operands.
  *
  * Common rules: block is 128, 256 or 512 (TFP8_E_BLOCK); rows at most 2^31 - 1, k a multiple of
- * block and at most 2^22 (TFP8_E_SIZE); ld >= k and lds >= k / block (TFP8_E_ARG), both at most
- * 2^22 (TFP8_E_SIZE); codes 16-byte aligned, ld a multiple of 16, alpha and scale 4 bytes, out the
+ * block and at most 2^22 (TFP8_E_SIZE); ld >= k and lds >= k / block (TFP8_E_ARG), ld at most 2^22
+ * and lds at most 2^20 (TFP8_E_SIZE); codes 16-byte aligned, ld a multiple of 16, alpha and scale 4 bytes, out the
  * size of an element, offsets 8 bytes (TFP8_E_ALIGN).  No output may overlap an input
  * (TFP8_E_ARG); inputs may overlap one another.  A product with no rows or no columns is a no-op;
  * with k = 0 it writes zeros.

@@ -47,7 +47,7 @@ def test_products_refuse_what_they_share(call):
     assert call(out=None) == -1
     assert call(a=put(A, 1, 496)) == -6 and call(b=put(B, 1, 511)) == -6
     assert call(a=put(A, 4, 3)) == -6 and call(b=put(B, 4, 3)) == -6
-    assert call(a=put(A, 1, (1 << 22) + 16)) == -2 and call(b=put(B, 4, (1 << 22) + 1)) == -2
+    assert call(a=put(A, 1, (1 << 22) + 16)) == -2 and call(b=put(B, 4, (1 << 20) + 1)) == -2
     assert call(a=put(A, 1, 520)) == -5 and call(a=put(A, 0, F + 8)) == -5
     assert call(b=put(B, 2, B[2] + 2)) == -5 and call(out=OUT + 1) == -5
     assert call(out=OUT + 2, dt=1) == -5
