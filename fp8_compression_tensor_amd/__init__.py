@@ -188,7 +188,19 @@ def matmul_grouped_t_raw(a, b, offsets_ptr: int, groups: int, rows: int, m: int,
 # ---------------------------------------------------------------------------- tensor wrappers
 
 def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+    # the raw handle of torch.cuda.current_stream(t.device), without making a Stream object
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _run(t: torch.Tensor, raw, *args):
+    """raw(*args) with t's device as the current one, and its status checked."""
+    if torch.cuda.current_device() == t.get_device():
+        status = raw(*args)
+    else:
+        with torch.cuda.device(t.device):
+            status = raw(*args)
+    if status != 0:
+        _check(status)
 
 
 def _need_gpu(*ts):
@@ -244,9 +256,8 @@ def compress(x: torch.Tensor, block: int = 128, target: float = 1.0, out=None, f
     _need_buf(codes, torch.uint8, n, "codes")
     _need_buf(alpha, torch.float32, nb, "alpha")
     _need_buf(scale, torch.float32, nb, "scale")
-    with torch.cuda.device(x.device):
-        _check(compress_raw(x.data_ptr(), dt, n, block, float(target), codes.data_ptr(),
-                            alpha.data_ptr(), scale.data_ptr(), _stream(x), flags))
+    _run(x, compress_raw, x.data_ptr(), dt, n, block, float(target), codes.data_ptr(),
+         alpha.data_ptr(), scale.data_ptr(), _stream(x), flags)
     return codes, alpha, scale
 
 
@@ -270,9 +281,8 @@ def decompress(codes: torch.Tensor, alpha: torch.Tensor, scale: torch.Tensor, bl
     else:
         _need_gpu(codes, out)
         _need_buf(out, dtype, n, "out")
-    with torch.cuda.device(codes.device):
-        _check(decompress_raw(codes.data_ptr(), alpha.data_ptr(), scale.data_ptr(), n, block,
-                              out.data_ptr(), dt, _stream(codes), flags))
+    _run(codes, decompress_raw, codes.data_ptr(), alpha.data_ptr(), scale.data_ptr(), n, block,
+         out.data_ptr(), dt, _stream(codes), flags)
     return out
 
 
@@ -328,17 +338,14 @@ def reduce_fp8(codes: torch.Tensor, alpha: torch.Tensor, scale: torch.Tensor, bl
         _need_buf(codes_out, torch.uint8, n, "codes_out")
         _need_buf(alpha_out, torch.float32, nb, "alpha_out")
         _need_buf(scale_out, torch.float32, nb, "scale_out")
-    with torch.cuda.device(codes.device):
-        if strided:
-            st = reduce_strided_raw(codes.data_ptr(), cst, alpha.data_ptr(), ast,
-                                    scale.data_ptr(), sst, P, n, block, float(target),
-                                    codes_out.data_ptr(), alpha_out.data_ptr(),
-                                    scale_out.data_ptr(), _stream(codes), flags)
-        else:
-            st = reduce_fp8_raw(codes.data_ptr(), alpha.data_ptr(), scale.data_ptr(), P, n, block,
-                                float(target), codes_out.data_ptr(), alpha_out.data_ptr(),
-                                scale_out.data_ptr(), _stream(codes), flags)
-        _check(st)
+    if strided:
+        _run(codes, reduce_strided_raw, codes.data_ptr(), cst, alpha.data_ptr(), ast,
+             scale.data_ptr(), sst, P, n, block, float(target), codes_out.data_ptr(),
+             alpha_out.data_ptr(), scale_out.data_ptr(), _stream(codes), flags)
+    else:
+        _run(codes, reduce_fp8_raw, codes.data_ptr(), alpha.data_ptr(), scale.data_ptr(), P, n,
+             block, float(target), codes_out.data_ptr(), alpha_out.data_ptr(),
+             scale_out.data_ptr(), _stream(codes), flags)
     return codes_out, alpha_out, scale_out
 
 
@@ -372,10 +379,9 @@ def accumulate(codes: torch.Tensor, alpha: torch.Tensor, scale: torch.Tensor, gr
         names = ("codes_out", "alpha_out", "scale_out")
         for t, ref, name in zip(out, (codes, alpha, scale), names):
             _need_buf(t, ref.dtype, ref.numel(), name)
-    with torch.cuda.device(codes.device):
-        _check(accumulate_raw(codes.data_ptr(), alpha.data_ptr(), scale.data_ptr(),
-                              grad.data_ptr(), dt, n, block, float(target), out[0].data_ptr(),
-                              out[1].data_ptr(), out[2].data_ptr(), _stream(codes), flags))
+    _run(codes, accumulate_raw, codes.data_ptr(), alpha.data_ptr(), scale.data_ptr(),
+         grad.data_ptr(), dt, n, block, float(target), out[0].data_ptr(), out[1].data_ptr(),
+         out[2].data_ptr(), _stream(codes), flags)
     return out
 
 
@@ -402,12 +408,12 @@ def _out_dtype(dtype: torch.dtype) -> int:
     raise ValueError(f"unsupported output dtype {dtype}")
 
 
-def _offsets_of(offsets: torch.Tensor, device: torch.device) -> int:
-    """The number of groups that offsets cut."""
+def _offsets_of(offsets: torch.Tensor, t: torch.Tensor) -> int:
+    """The number of groups that offsets cut, on t's device."""
     if not (isinstance(offsets, torch.Tensor) and offsets.is_cuda):
         raise ValueError("tfp8 operates on GPU tensors only (no CPU path)")
-    if offsets.device != device:
-        raise ValueError(f"tensors on different devices ({device} and {offsets.device})")
+    if offsets.get_device() != t.get_device():
+        raise ValueError(f"tensors on different devices ({t.device} and {offsets.device})")
     if offsets.dtype != torch.int64 or offsets.dim() != 1 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int64 vector")
     groups = offsets.numel() - 1
@@ -417,12 +423,23 @@ def _offsets_of(offsets: torch.Tensor, device: torch.device) -> int:
 
 
 def _operand(t, block: int, dims: int, name: str):
-    """(codes, alpha, scale) of an operand -> (shape of codes, its raw form, device).
+    """(codes, alpha, scale) of an operand -> (shape of codes, its raw form).
 
     codes is uint8 [rows, k] (dims = 2, rows at any stride that is a multiple of 16) or contiguous
     [groups, rows, k]; alpha and scale are float32 with k / block values a row, [rows, k / block]
     with contiguous rows, or contiguous in any shape (as compress returns them)."""
     codes, alpha, scale = t
+    # the common form, all contiguous, in the order of what costs least; whatever fails here is
+    # looked at again below
+    if (isinstance(codes, torch.Tensor) and isinstance(alpha, torch.Tensor)
+            and isinstance(scale, torch.Tensor) and codes.dim() == dims and codes.dtype == torch.uint8 and codes.is_contiguous()
+            and alpha.dtype == scale.dtype == torch.float32 and alpha.is_contiguous()
+            and scale.is_contiguous()
+            and codes.get_device() == alpha.get_device() == scale.get_device() >= 0):
+        k, n = codes.shape[-1], codes.numel()
+        if k % block == 0 and alpha.numel() == scale.numel() == n // block:
+            nb = k // block
+            return codes.shape, (codes.data_ptr(), k, alpha.data_ptr(), scale.data_ptr(), nb)
     for x, dt, what in ((codes, torch.uint8, "codes"), (alpha, torch.float32, "alpha"),
                         (scale, torch.float32, "scale")):
         if not (isinstance(x, torch.Tensor) and x.is_cuda):
@@ -456,11 +473,14 @@ def _operand(t, block: int, dims: int, name: str):
             raise ValueError(f"{what} of {name} must be [{rows}, {nb}] with contiguous rows")
     if strides[0] != strides[1]:
         raise ValueError(f"alpha and scale of {name} must have the same row stride")
-    return codes.shape, (codes.data_ptr(), ld, alpha.data_ptr(), scale.data_ptr(),
-                         strides[0]), codes.device
+    return codes.shape, (codes.data_ptr(), ld, alpha.data_ptr(), scale.data_ptr(), strides[0])
 
 
-def _product_out(out, shape, dtype: torch.dtype, device: torch.device):
+def _product_out(out, shape, dtype: torch.dtype, a, b):
+    """The output, new or checked, of a product of a and b, whose devices are compared."""
+    device = a[0].device
+    if device != b[0].device:
+        raise ValueError(f"tensors on different devices ({device} and {b[0].device})")
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not (isinstance(out, torch.Tensor) and out.is_cuda):
@@ -503,24 +523,24 @@ def compress_t(x: torch.Tensor, block: int = 128, target: float = 1.0, offsets=N
     if rows and cols > 1 and x.stride(1) != 1:
         raise ValueError("the rows of x must be contiguous")
     ldx = x.stride(0) if rows > 1 else cols
-    groups = 1 if offsets is None else _offsets_of(offsets, x.device)
+    groups = 1 if offsets is None else _offsets_of(offsets, x)
     kp = padded_rows(rows, groups, block)
     if out is None:
         out = (torch.empty((cols, kp), dtype=torch.uint8, device=x.device),
                torch.empty((cols, kp // block), dtype=torch.float32, device=x.device),
                torch.empty((cols, kp // block), dtype=torch.float32, device=x.device))
-    codes, alpha, scale = out
-    _need_gpu(codes, alpha, scale)
-    if codes.device != x.device:
-        raise ValueError(f"tensors on different devices ({x.device} and {codes.device})")
-    _need_buf(codes, torch.uint8, cols * kp, "codes")
-    _need_buf(alpha, torch.float32, cols * (kp // block), "alpha")
-    _need_buf(scale, torch.float32, cols * (kp // block), "scale")
-    with torch.cuda.device(x.device):
-        _check(compress_t_raw(x.data_ptr(), dt, rows, cols, ldx,
-                              None if offsets is None else offsets.data_ptr(), groups, block,
-                              float(target), codes.data_ptr(), alpha.data_ptr(),
-                              scale.data_ptr(), _stream(x), flags))
+        codes, alpha, scale = out
+    else:
+        codes, alpha, scale = out
+        _need_gpu(codes, alpha, scale)
+        if codes.device != x.device:
+            raise ValueError(f"tensors on different devices ({x.device} and {codes.device})")
+        _need_buf(codes, torch.uint8, cols * kp, "codes")
+        _need_buf(alpha, torch.float32, cols * (kp // block), "alpha")
+        _need_buf(scale, torch.float32, cols * (kp // block), "scale")
+    _run(x, compress_t_raw, x.data_ptr(), dt, rows, cols, ldx,
+         None if offsets is None else offsets.data_ptr(), groups, block, float(target),
+         codes.data_ptr(), alpha.data_ptr(), scale.data_ptr(), _stream(x), flags)
     return codes, alpha, scale
 
 
@@ -530,16 +550,12 @@ def matmul(a, b, block: int = 128, dtype: torch.dtype = torch.bfloat16, out=None
     bfloat16."""
     _product_block(block)
     dt = _out_dtype(dtype)
-    (m, k), ra, dev = _operand(a, block, 2, "a")
-    (n, kb), rb, devb = _operand(b, block, 2, "b")
+    (m, k), ra = _operand(a, block, 2, "a")
+    (n, kb), rb = _operand(b, block, 2, "b")
     if k != kb:
         raise ValueError(f"a and b have rows of {k} and {kb} elements")
-    if dev != devb:
-        raise ValueError(f"tensors on different devices ({dev} and {devb})")
-    out = _product_out(out, (m, n), dtype, dev)
-    with torch.cuda.device(dev):
-        _check(matmul_raw(ra, rb, m, n, k, block, out.data_ptr(), dt, _out_rows(out),
-                          _stream(out)))
+    out = _product_out(out, (m, n), dtype, a, b)
+    _run(out, matmul_raw, ra, rb, m, n, k, block, out.data_ptr(), dt, _out_rows(out), _stream(out))
     return out
 
 
@@ -550,19 +566,16 @@ def matmul_grouped(a, b, offsets: torch.Tensor, block: int = 128,
     group's b.  Rows past offsets[-1] become zeros."""
     _product_block(block)
     dt = _out_dtype(dtype)
-    (m, k), ra, dev = _operand(a, block, 2, "a")
-    (g, n, kb), rb, devb = _operand(b, block, 3, "b")
+    (m, k), ra = _operand(a, block, 2, "a")
+    (g, n, kb), rb = _operand(b, block, 3, "b")
     if k != kb:
         raise ValueError(f"a and b have rows of {k} and {kb} elements")
-    if dev != devb:
-        raise ValueError(f"tensors on different devices ({dev} and {devb})")
-    groups = _offsets_of(offsets, dev)
+    groups = _offsets_of(offsets, a[0])
     if groups != g:
         raise ValueError(f"offsets cut {groups} groups and b holds {g}")
-    out = _product_out(out, (m, n), dtype, dev)
-    with torch.cuda.device(dev):
-        _check(matmul_grouped_raw(ra, rb, offsets.data_ptr(), groups, m, n, k, block,
-                                  out.data_ptr(), dt, _out_rows(out), _stream(out)))
+    out = _product_out(out, (m, n), dtype, a, b)
+    _run(out, matmul_grouped_raw, ra, rb, offsets.data_ptr(), groups, m, n, k, block,
+         out.data_ptr(), dt, _out_rows(out), _stream(out))
     return out
 
 
@@ -573,18 +586,15 @@ def matmul_grouped_t(a, b, offsets: torch.Tensor, rows: int, block: int = 128,
     a of dY and b of X: each expert's weight gradient).  Zeros for an empty group."""
     _product_block(block)
     dt = _out_dtype(dtype)
-    (m, k), ra, dev = _operand(a, block, 2, "a")
-    (n, kb), rb, devb = _operand(b, block, 2, "b")
-    if dev != devb:
-        raise ValueError(f"tensors on different devices ({dev} and {devb})")
-    groups = _offsets_of(offsets, dev)
+    (m, k), ra = _operand(a, block, 2, "a")
+    (n, kb), rb = _operand(b, block, 2, "b")
+    groups = _offsets_of(offsets, a[0])
     kp = padded_rows(rows, groups, block)
     if k != kp or kb != kp:
         raise ValueError(f"{rows} rows in {groups} groups are {kp} elements a row, got {k} and {kb}")
-    out = _product_out(out, (groups, m, n), dtype, dev)
+    out = _product_out(out, (groups, m, n), dtype, a, b)
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")
-    with torch.cuda.device(dev):
-        _check(matmul_grouped_t_raw(ra, rb, offsets.data_ptr(), groups, rows, m, n, block,
-                                    out.data_ptr(), dt, _stream(out)))
+    _run(out, matmul_grouped_t_raw, ra, rb, offsets.data_ptr(), groups, rows, m, n, block,
+         out.data_ptr(), dt, _stream(out))
     return out

@@ -109,17 +109,26 @@ __device__ __forceinline__ void mfma_row(f32x4 (&part)[N], const Fragment<true> 
                                                         0);
     }
 }
+template <int N>
+__device__ __forceinline__ void mfma_row(f32x4 (&part)[N], const Fragment<false> (&x)[N],
+                                         const Fragment<false> &y) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    part[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x[j].v, y.v, zero, 0, 0, 0, 0, 0, 0);
+  }
+}
 __device__ __forceinline__ f32x4 mfma_codes(const Fragment<false> &x, const Fragment<false> &y) {
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.v, y.v, zero, 0, 0, 0, 0, 0, 0);
 }
 
 // A raw buffer descriptor: reads at or past `bytes` give zeros.
-__device__ __forceinline__ i32x4 buffer_of(const void *base, int64_t bytes) {
+__device__ __forceinline__ i32x4 buffer_of(const void *base, int bytes) {
   const uint64_t p = (uint64_t)base;
   return i32x4{__builtin_amdgcn_readfirstlane((int)p),
                __builtin_amdgcn_readfirstlane((int)(p >> 32) & 0xFFFF),
-               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+               __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
 }
 
 // 16 bytes a lane from the buffer at offset voff + soff to LDS, lane l's at to + 16 l.  Written as
@@ -137,43 +146,77 @@ __device__ __forceinline__ void load_to_lds(i32x4 buffer, int voff, int soff, co
       : "memory");
 }
 // Every load of this wavefront, to registers or to LDS, has arrived.
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-// Every LDS access of this wavefront is done, then those of the whole workgroup.
+// All but the last N.
+template <int N = 0>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Every LDS access of this wavefront is done,
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// and those of the whole workgroup.
 __device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  wait_lds();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
+// Vectors that may start at any element (global memory takes them at any address).
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) |
+         ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16);
+}
+
+// Four neighbouring values of a row, of which the first `valid` are inside.
 template <bool F32OUT>
-__device__ __forceinline__ void store_values(void *out, int64_t at, const f32x4 v, int valid,
-                                             bool wide) {
+__device__ __forceinline__ void store_values(void *out, int64_t at, const f32x4 v, int valid) {
   if constexpr (F32OUT) {
     float *o = (float *)out + at;
-    if (wide && valid >= 4) {
-      *(f32x4 *)o = v;
+    if (valid >= 4) {
+      *(f32x4u *)o = v;
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 3; ++i)
         if (i < valid) o[i] = v[i];
     }
   } else {
     __bf16 *o = (__bf16 *)out + at;
-    __bf16 h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = (__bf16)v[i];
-    if (wide && valid >= 4) {
-      u32x2 w;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        w[i] = (uint32_t)__builtin_bit_cast(uint16_t, h[2 * i]) |
-               ((uint32_t)__builtin_bit_cast(uint16_t, h[2 * i + 1]) << 16);
-      *(u32x2 *)o = w;
+    if (valid >= 4) {
+      *(u32x2_any *)o = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < valid) o[i] = h[i];
+      for (int i = 0; i < 3; ++i)
+        if (i < valid) o[i] = (__bf16)v[i];
     }
+  }
+}
+
+// A row of two neighbouring 16 x 16 tiles in bfloat16.  The lanes q = 0..3 of a row hold columns 4 q
+// on of each tile (8 bytes); two swaps between lanes 32 and 16 apart give lane q columns 8 q on of
+// the 32, so that the four store 64 bytes together.  (4096 x 4096 x 1024: 25.8 us, against
+// 29.4 in pieces of 8 bytes.)
+__device__ __forceinline__ void store_pair(void *out, int64_t at, int q, f32x4 a, f32x4 b,
+                                           int valid) {
+  uint32_t x[2] = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
+  uint32_t y[2] = {pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto s = __builtin_amdgcn_permlane32_swap(x[i], y[i], false, false);
+    const auto u = __builtin_amdgcn_permlane16_swap(s[0], s[1], false, false);
+    x[i] = u[0];
+    y[i] = u[1];
+  }
+  __bf16 *o = (__bf16 *)out + at + 8 * q;
+  valid -= 8 * q;
+  const uint32_t d[4] = {x[0], x[1], y[0], y[1]};
+  if (valid >= 8) {
+    *(u32x4_any *)o = u32x4{d[0], d[1], d[2], d[3]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < valid) ((uint16_t *)o)[i] = (uint16_t)(d[i / 2] >> (16 * (i & 1)));
   }
 }
 
@@ -196,28 +239,27 @@ constexpr int kBand = 4;
 
 template <int BM, int BN, int MODE, int ES>
 __device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
-  int64_t bid = blockIdx.x;
+  uint32_t bid = blockIdx.x;
   if constexpr (MODE != kGroupedDepth) {
-    const unsigned per = gridDim.x >> 3, over = gridDim.x & 7, x = blockIdx.x & 7;
+    const uint32_t per = gridDim.x >> 3, over = gridDim.x & 7, x = blockIdx.x & 7;
     bid = x * per + (x < over ? x : over) + (blockIdx.x >> 3);
   }
   char *out = (char *)p.out;
   int64_t s0 = 0, s1 = p.steps;
   if constexpr (MODE == kGroupedDepth) {
-    const int per = p.mtiles * p.ntiles;
-    const int e = (int)(bid / per);
-    bid -= (int64_t)e * per;
-    const GroupSpan g = span_of_group(p.offsets, p.groups, p.rows, kStep << p.shift, e);
+    const uint32_t per = (uint32_t)p.mtiles * p.ntiles, e = bid / per;
+    bid -= e * per;
+    const GroupSpan g = span_of_group(p.offsets, p.groups, p.rows, kStep << p.shift, (int)e);
     s0 = g.unit0 << p.shift;
     s1 = (g.unit0 + g.units) << p.shift;
     s1 = s1 < p.steps ? s1 : p.steps;
     s0 = s0 < s1 ? s0 : s1;
     out += (int64_t)e * p.next_c * ES;
   }
-  const int band = kBand * p.ntiles;
-  const int b0 = (int)(bid / band) * kBand, in_band = (int)(bid % band);
-  const int high = p.mtiles - b0 < kBand ? p.mtiles - b0 : kBand;
-  const int mt = b0 + in_band % high, nt = in_band / high;
+  const uint32_t band = kBand * (uint32_t)p.ntiles, in_band = bid % band;
+  const int b0 = (int)(bid / band) * kBand;
+  const uint32_t high = p.mtiles - b0 < kBand ? p.mtiles - b0 : kBand;
+  const int mt = b0 + (int)(in_band % high), nt = (int)(in_band / high);
   const int64_t n0 = (int64_t)nt * BN;
   int64_t m0, bskip = 0, bskip_s = 0;
   if constexpr (MODE == kGroupedRows) {
@@ -248,23 +290,26 @@ __device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
   return true;
 }
 
-// LDS of a tile: two stages of a step's codes, A's rows then B's, and their scales r.
-template <int BM, int BN>
+// LDS of a tile: NS stages of a step's codes, A's rows then B's, and scales r: those of a step for
+// each stage, or (CHUNK > 0) those of CHUNK blocks.
+template <int BM_, int BN_, int NS_, int CHUNK_>
 struct Stages {
-  alignas(1024) uint8_t codes[2][(BM + BN) * kStep];
-  float r[2][BM + BN];
+  static constexpr int BM = BM_, BN = BN_, NS = NS_, CHUNK = CHUNK_;
+  alignas(1024) uint8_t codes[NS][(BM + BN) * kStep];
+  float r[CHUNK ? CHUNK : NS][BM + BN];
 };
 
 // Filling the stages.
-template <int BM, int BN, int NW>
+template <class STAGES, int NW>
 struct Feed {
+  static constexpr int BM = STAGES::BM, BN = STAGES::BN, CHUNK = STAGES::CHUNK;
   static constexpr int ROWS = BM + BN, NT = 64 * NW;
   static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // a wavefront's loads a step
   static constexpr int SC = (ROWS + NT - 1) / NT;           // rows whose scales a thread prepares
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole loads of one operand");
   static_assert(BM % 64 == 0 && ROWS % 64 == 0, "a wavefront's scales are of one operand");
 
-  Stages<BM, BN> &lds;
+  STAGES &lds;
   int w, shift, first, blocks;
   i32x4 ra[LA], rb[LB];
   int va, vb;
@@ -276,25 +321,23 @@ struct Feed {
   // takes them from chunk (i & 7) ^ (row & 7) of its row, so that the lanes that read a column of
   // fragments touch all banks.  Each instruction has a descriptor of its own, from its first row on
   // to the operand's end, past which rows read as zeros.
-  __device__ __forceinline__ Feed(Stages<BM, BN> &l, const ProductArgs &p, const Job &t)
+  __device__ __forceinline__ Feed(STAGES &l, const ProductArgs &p, const Job &t)
       : lds(l), shift(p.shift) {
     const int tid = threadIdx.x, lane = tid & 63;
     w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
     va = (lane >> 3) * (int)p.a.ld + chunk;
     vb = (lane >> 3) * (int)p.b.ld + chunk;
-    const int64_t k = p.steps * kStep;
+    const int k = (int)p.steps * kStep, lda = (int)p.a.ld, ldb = (int)p.b.ld;  // products < 2^31
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-      const int row = (i * NW + w) * 8;
-      const int64_t left = (int64_t)(t.mv - 1 - row) * p.a.ld + k;
-      ra[i] = buffer_of(t.ac + (int64_t)row * p.a.ld, left > 0 ? left : 0);
+      const int row = (i * NW + w) * 8, left = (t.mv - 1 - row) * lda + k;
+      ra[i] = buffer_of(t.ac + row * lda, left > 0 ? left : 0);
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
-      const int row = (i * NW + w) * 8;
-      const int64_t left = (int64_t)(t.nv - 1 - row) * p.b.ld + k;
-      rb[i] = buffer_of(t.bc + (int64_t)row * p.b.ld, left > 0 ? left : 0);
+      const int row = (i * NW + w) * 8, left = (t.nv - 1 - row) * ldb + k;
+      rb[i] = buffer_of(t.bc + row * ldb, left > 0 ? left : 0);
     }
 #pragma unroll
     for (int i = 0; i < SC; ++i) {
@@ -322,10 +365,48 @@ struct Feed {
                     &lds.codes[stage][BM * kStep + ((i - LA) * NW + w) * 1024]);
     }
   }
-  // Scales: thread t prepares r = scale / alpha of row t (A's rows, then B's).  They lie a row
-  // apart in memory, a cache line each, so four blocks' are loaded at once: called for every
-  // step, this loads at the first of four blocks.
+  // Scales, r = scale / alpha of every row (A's, then B's).
+  //
+  // CHUNK > 0: the next CHUNK blocks' at once, from block b on, four to a thread.
+  __device__ __forceinline__ void fill_scales(int b, const ProductArgs &p, const Job &t) {
+    constexpr int QUADS = CHUNK / 4, EACH = ROWS * QUADS / NT;
+    static_assert(CHUNK % 4 == 0 && ROWS * QUADS % NT == 0, "whole quads for every thread");
+    f32x4 x[EACH], y[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const int at = (int)threadIdx.x + i * NT, row = at / QUADS, k = b + at % QUADS * 4;
+      const bool isa = row < BM;
+      int rr = isa ? row : row - BM;
+      const int last = (isa ? t.mv : t.nv) - 1;
+      rr = rr < last ? rr : last;
+      const int64_t from = (int64_t)rr * (isa ? p.a.lds : p.b.lds) + k;
+      const float *ss = (isa ? t.as : t.bs) + from, *aa = (isa ? t.aa : t.ba) + from;
+      x[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      y[i] = f32x4{1.0f, 1.0f, 1.0f, 1.0f};
+      if (k + 4 <= blocks) {
+        x[i] = *(const f32x4u *)ss;
+        y[i] = *(const f32x4u *)aa;
+      } else {
+#pragma unroll
+        for (int u = 0; u < 3; ++u)
+          if (k + u < blocks) {
+            x[i][u] = ss[u];
+            y[i][u] = aa[u];
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const int at = (int)threadIdx.x + i * NT, row = at / QUADS, k = at % QUADS * 4;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) lds.r[k + u][row] = x[i][u] * __builtin_amdgcn_rcpf(y[i][u]);
+    }
+  }
+  // CHUNK = 0: thread t prepares row t's.  Rows' lie a row apart in memory, a cache line each, so
+  // four blocks' are loaded at once: called for every step, this loads at the first of four
+  // blocks.
   __device__ __forceinline__ void load_scales(int s) {
+    if constexpr (CHUNK > 0) return;
     const int at = s >> shift;
     if (((at - first) & 3) || (s & ((1 << shift) - 1))) return;
 #pragma unroll
@@ -344,6 +425,7 @@ struct Feed {
     }
   }
   __device__ __forceinline__ void put_scales(int s, int stage) {
+    if constexpr (CHUNK > 0) return;
     const int k = ((s >> shift) - first) & 3;
 #pragma unroll
     for (int i = 0; i < SC; ++i) {
@@ -369,24 +451,42 @@ __device__ __forceinline__ Fragment<WIDE> read_fragment(const uint8_t *codes, in
 // The loop over steps, for wavefronts of TM x TN tiles.  The scaled addition of a tile's partial
 // products follows TN matrix instructions behind the one that makes them, so that neither waits for
 // the other.  One barrier a step, before the last row of tiles: by then the step's fragments are in
-// registers, so the loads of the step after next may overwrite them, and the next step's first
+// registers, so the loads of the step NS ahead may overwrite them, and the next step's first
 // fragments are read under the last row's products.
-template <int BM, int BN, int TM, int TN, bool WIDE, class FEED>
-__device__ __forceinline__ void run_steps(Stages<BM, BN> &lds, FEED &feed, int s0, int s1,
-                                          int mrow, int nrow, f32x4 (&acc)[TM][TN]) {
+template <int TM, int TN, bool WIDE, class STAGES, class FEED>
+__device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const ProductArgs &p,
+                                          const Job &job, int mrow, int nrow,
+                                          f32x4 (&acc)[TM][TN]) {
+  constexpr int NS = STAGES::NS, BM = STAGES::BM, CHUNK = STAGES::CHUNK;
+  constexpr int NP = TM >= 8 ? 3 : TM >= 3 ? 2 : 1;  // a step's loads go out in this many shares
+  constexpr int LOADS = FEED::LA + FEED::LB;
+  const int s0 = job.s0, s1 = job.s1;
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
   const int fa0 = fragment_offset(mrow, q, l16), fb0 = fragment_offset(BM + nrow, q, l16);
-  constexpr int NP = TM >= 8 ? 3 : 2;  // a step's loads go out in this many shares
   int s = s0;
-  feed.load_step(s, 0);
+  int chunk0 = s0 >> p.shift;  // first block of the scales in LDS (CHUNK)
+  // With more than two stages every step issues its loads, past the end those of the last step
+  // again, so that the number in flight is always the same.
+  const auto load = [&](int x, int slot, int part, int parts) {
+    if (NS > 2)
+      feed.load_step(x < s1 ? x : s1 - 1, slot, part, parts);
+    else if (x < s1)
+      feed.load_step(x, slot, part, parts);
+  };
   feed.load_scales(s);
-  wait_loads();
+#pragma unroll
+  for (int k = 0; k < NS - 1; ++k) load(s + k, k, 0, 1);
+  if (NS == 2) wait_loads();
   feed.put_scales(s, 0);
+  if constexpr (CHUNK > 0) feed.fill_scales(chunk0, p, job);
+  wait_loads<(NS - 2) * LOADS>();
   lds_barrier();
-  if (s + 1 < s1) {
-    feed.load_step(s + 1, 1, 0, NP);
-    if (NP == 1) feed.load_scales(s + 1);
-  }
+  load(s + NS - 1, NS - 1, 0, NP);
+  if (NP == 1 && s + 1 < s1) feed.load_scales(s + 1);
+  // where the scales of step x, in slot y, are
+  const auto scales = [&](int x, int y) {
+    return CHUNK > 0 ? lds.r[((x < s1 ? x : s1 - 1) >> p.shift) - chunk0] : lds.r[y];
+  };
   Fragment<WIDE> fb[TN], fa;
   f32x4 rb[TN], part[TN];
   float ra, rprev = 0.0f;  // A's scales of this row of tiles and of the one before
@@ -396,7 +496,7 @@ __device__ __forceinline__ void run_steps(Stages<BM, BN> &lds, FEED &feed, int s
     rb[j] = part[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   fa = read_fragment<WIDE>(lds.codes[0], fa0);
-  ra = lds.r[0][mrow + l16];
+  ra = scales(s, 0)[mrow + l16];
   // part[j] of the row of tiles before, scaled and added
   auto add_part = [&](f32x4 (&to)[TN], int j) {
 #pragma unroll
@@ -405,29 +505,37 @@ __device__ __forceinline__ void run_steps(Stages<BM, BN> &lds, FEED &feed, int s
     // every partial product until then
     asm volatile("" : "+v"(to[j]));
   };
-  for (int stage = 0; s < s1; ++s, stage ^= 1) {
+  const auto next = [](int slot) { return NS == 2 ? slot ^ 1 : slot + 1 < NS ? slot + 1 : 0; };
+  for (int slot = 0; s < s1; ++s, slot = next(slot)) {
+    const int ahead = next(slot);
+    const int back = NS == 2 ? ahead : slot ? slot - 1 : NS - 1;  // of the step NS - 1 ahead
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const bool last = i == TM - 1;
       if (last) {
-        wait_loads();
-        if (s + 1 < s1) feed.put_scales(s + 1, stage ^ 1);
+        wait_loads<(NS - 2) * LOADS>();
+        if (s + 1 < s1) feed.put_scales(s + 1, ahead);
         lds_barrier();
-        if (s + 2 < s1) {
-          feed.load_step(s + 2, stage, 0, NP);
-          if (NP == 1) feed.load_scales(s + 2);
+        load(s + NS, slot, 0, NP);
+        if (NP == 1 && s + 2 < s1) feed.load_scales(s + 2);
+        if constexpr (CHUNK > 0) {
+          if (s + 1 < s1 && ((s + 1) >> p.shift) - chunk0 == CHUNK) {
+            chunk0 += CHUNK;
+            feed.fill_scales(chunk0, p, job);
+            lds_barrier();
+          }
         }
-      } else if (i + 1 < NP && s + 1 < s1) {
-        feed.load_step(s + 1, stage ^ 1, i + 1, NP);
-        if (i + 2 == NP) feed.load_scales(s + 1);
+      } else if (i + 1 < NP) {
+        load(s + NS - 1, back, i + 1, NP);
+        if (i + 2 == NP && s + 1 < s1) feed.load_scales(s + 1);
       }
-      const int ns = last ? stage ^ 1 : stage;
+      const int ns = last ? ahead : slot;
       const int ni = last ? 0 : i + 1;
       const Fragment<WIDE> fn = read_fragment<WIDE>(lds.codes[ns], fa0 + ni * 16 * kStep);
-      const float rn = lds.r[ns][mrow + ni * 16 + l16];
+      const float rn = scales(last ? s + 1 : s, ns)[mrow + ni * 16 + l16];
       // B's scales of this step replace the last one's once its last row is added
       auto next_scales = [&](int j) {
-        if (i == 0) rb[j] = *(const f32x4 *)&lds.r[stage][BM + nrow + j * 16 + 4 * q];
+        if (i == 0) rb[j] = *(const f32x4 *)&scales(s, slot)[BM + nrow + j * 16 + 4 * q];
       };
       if constexpr (WIDE) {
 #pragma unroll
@@ -456,14 +564,16 @@ __device__ __forceinline__ void run_steps(Stages<BM, BN> &lds, FEED &feed, int s
   }
 #pragma unroll
   for (int j = 0; j < TN; ++j) add_part(acc[TM - 1], j);
+  if (NS > 2) wait_loads();  // no load may arrive after the workgroup has given its LDS back
 }
 
 // The kernel only calls this function: a kernel's own body is also read by the host's pass, which
 // does not know these builtins.
-template <int BM, int BN, int WM, int WN, int MODE, bool F32OUT>
+template <int BM, int BN, int WM, int WN, int NS, int CHUNK, int MODE, bool F32OUT>
 __device__ __forceinline__ void matmul_tile(const ProductArgs &p) {
   constexpr int TM = BM / 16 / WM, TN = BN / 16 / WN;
-  __shared__ Stages<BM, BN> lds;
+  using STAGES = Stages<BM, BN, NS, CHUNK>;
+  __shared__ STAGES lds;
   Job t;
   if (!find_job<BM, BN, MODE, F32OUT ? 4 : 2>(p, t)) return;
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
@@ -475,176 +585,225 @@ __device__ __forceinline__ void matmul_tile(const ProductArgs &p) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   if (t.s0 < t.s1) {
-    Feed<BM, BN, WM * WN> feed(lds, p, t);
-    run_steps<BM, BN, TM, TN, F32OUT>(lds, feed, t.s0, t.s1, mrow, nrow, acc);
+    Feed<STAGES, WM * WN> feed(lds, p, t);
+    run_steps<TM, TN, F32OUT>(lds, feed, p, t, mrow, nrow, acc);
   }
-  const bool wide = ((uintptr_t)t.out % (F32OUT ? 16 : 8) == 0) && (p.ldc % 4 == 0);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int row = mrow + i * 16 + l16;
-    if (row < t.mv) {
+    if constexpr (F32OUT) {
+      if (row < t.mv) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int col = nrow + j * 16 + 4 * q;
-        store_values<F32OUT>(t.out, row * p.ldc + col, acc[i][j], t.nv - col, wide);
+        for (int j = 0; j < TN; ++j) {
+          const int col = nrow + j * 16 + 4 * q;
+          store_values<true>(t.out, row * p.ldc + col, acc[i][j], t.nv - col);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < TN; j += 2) {  // every lane takes part in the swaps
+        const int col = nrow + j * 16;
+        store_pair(t.out, row * p.ldc + col, q, acc[i][j], acc[i][j + 1],
+                   row < t.mv ? t.nv - col : 0);
       }
     }
   }
 }
 
-template <int BM, int BN, int WM, int WN, int MODE, bool F32OUT>
+template <int BM, int BN, int WM, int WN, int NS, int CHUNK, int MODE, bool F32OUT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_matmul_tile(ProductArgs p) {
-  matmul_tile<BM, BN, WM, WN, MODE, F32OUT>(p);
+  matmul_tile<BM, BN, WM, WN, NS, CHUNK, MODE, F32OUT>(p);
 }
 
 // --------------------------------------------------------------------------------------------
-// Few rows (decoding): the product reads B once and is bound by that, so it keeps as many of its
-// bytes in flight as it can and shares nothing.  A workgroup takes 16 MT rows of A (its group's) and
-// 16 TN of B; its eight wavefronts take turns at chunks of four steps, reading the fragments straight
-// from memory into registers (lane l: chunks q and q + 4 of row l & 15, so that an instruction's four
-// lanes of a row take 64 bytes of it), and add up through LDS in a fixed order at the end.  A's
-// scales are prepared in LDS for the whole depth first, B's are read four blocks at a time.  Products
-// are of rows of A by rows of B here: D[4 q + i][l & 15] is row m = 4 q + i and column n = l & 15, so
-// that a lane needs one scale of B.
-constexpr int kFewWaves = 8, kFewChunk = 4;
-constexpr int kFewScales = 8192;  // scales of A that fit: rows of a workgroup times blocks of a row
+// Products too small to fill the chip with tiles whose wavefronts share them: few rows (decoding,
+// where B's bytes bound the product) or few tiles.  A workgroup takes one tile of 16 MT rows of A
+// (its group's) by 16 TN of B, and its eight wavefronts divide the depth: each computes the whole tile
+// over its share of the steps, and the eight are added up through LDS in a fixed order at the end.
+// Each wavefront has ST stages of LDS to itself, so there is no barrier in the loop: it waits for
+// its own loads alone, reads a step's fragments into registers, and sends the stage's next loads
+// out before it multiplies.  (Fragments loaded straight from memory, 16 rows of 64 bytes an
+// instruction in the order of the lanes, come at 9.6 TB/s over the chip, from the L1 cache too; whole
+// lines through LDS come at 28.)  With one stage, the next step's fragments are read under this
+// one's products.  Scales are prepared in LDS, kSplitBlocks blocks at a time.
+constexpr int kSplitWaves = 8, kSplitBlocks = 64;
 
-template <bool WIDE>
-__device__ __forceinline__ Fragment<WIDE> load_fragment(const uint8_t *row, int q) {
-  return make_fragment<WIDE>(*(const u32x4 *)(row + q * 16), *(const u32x4 *)(row + q * 16 + 64));
-}
-__device__ __forceinline__ f32x4 mfma_one(const Fragment<false> &x, const Fragment<false> &y) {
-  return mfma_codes(x, y);
-}
-__device__ __forceinline__ f32x4 mfma_one(const Fragment<true> &x, const Fragment<true> &y) {
-  f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.v[t], y.v[t], d, 0, 0, 0);
-  return d;
+// 32 codes of a lane, as stored.
+struct Codes {
+  u32x4 lo, hi;
+};
+__device__ __forceinline__ Codes read_codes(const uint8_t *codes, int at) {
+  return Codes{*(const u32x4 *)(codes + at), *(const u32x4 *)(codes + (at ^ 64))};
 }
 
-template <int MT, int TN, int MODE, bool F32OUT>
-__device__ __forceinline__ void matmul_few(const ProductArgs &p) {
-  constexpr int BM = 16 * MT, BN = 16 * TN;
-  __shared__ union {
-    float r[kFewScales];                          // A's scales, [row][block]
-    float sum[kFewWaves][MT * TN][16][17];        // the wavefronts' sums
+template <int MT, int TN, int ST, int MODE, bool F32OUT>
+__device__ __forceinline__ void matmul_split(const ProductArgs &p) {
+  constexpr int BM = 16 * MT, BN = 16 * TN, ROWS = BM + BN, NT = 64 * kSplitWaves;
+  constexpr int QUADS = kSplitBlocks / 4, EACH = (ROWS * QUADS + NT - 1) / NT;
+  constexpr int LOADS = ROWS / 8;  // a step's
+  __shared__ struct {
+    union {
+      alignas(1024) uint8_t codes[kSplitWaves][ST][ROWS * kStep];
+      f32x4 sum[kSplitWaves][MT * TN][64];
+    };
+    float r[kSplitBlocks][ROWS];
   } lds;
+  Job t;
+  if (!find_job<BM, BN, MODE, F32OUT ? 4 : 2>(p, t)) return;
   const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, l16 = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int mt = (int)(blockIdx.x % p.mtiles), nt = (int)(blockIdx.x / p.mtiles);
-  const int64_t n0 = (int64_t)nt * BN;
-  int64_t m0 = (int64_t)mt * BM, bskip = 0, bskip_s = 0;
-  int mv, steps = (int)p.steps;
-  if constexpr (MODE == kGroupedRows) {
-    const GroupTile g = tile_of_groups(p.offsets, p.groups, p.m, BM, mt, p.groups);
-    if (g.rows <= 0) return;
-    m0 = g.row0;
-    mv = g.rows;
-    if (g.group == p.groups) {  // rows past the last group: zeros
-      steps = 0;
-    } else {
-      bskip = (int64_t)g.group * p.b.next;
-      bskip_s = (int64_t)g.group * p.b.next_s;
-    }
-  } else {
-    mv = (int)(p.m - m0 < BM ? p.m - m0 : BM);
-  }
-  const int nv = (int)(p.n - n0 < BN ? p.n - n0 : BN);
-  const int blocks = steps >> p.shift;
 
-  // the rows of this lane's fragments; past the end, the last row again
-  const uint8_t *ar[MT], *br[TN];
-  const float *ba[TN], *bs[TN];
+  // loads: 8 rows each, as in Feed
+  i32x4 from[LOADS];
+  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  const int va = (lane >> 3) * (int)p.a.ld + chunk, vb = (lane >> 3) * (int)p.b.ld + chunk;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int row = i * 16 + l16 < mv ? i * 16 + l16 : mv - 1;
-    ar[i] = p.a.codes + (m0 + row) * p.a.ld;
+  for (int i = 0; i < LOADS; ++i) {
+    const bool isa = i < BM / 8;
+    const int row = isa ? i * 8 : i * 8 - BM;
+    const int ld = (int)(isa ? p.a.ld : p.b.ld);  // below 2^22, and at most 64 rows
+    const int left = ((isa ? t.mv : t.nv) - 1 - row) * ld + (int)p.steps * kStep;
+    from[i] = buffer_of((isa ? t.ac : t.bc) + row * ld, left > 0 ? left : 0);
   }
+  const auto load = [&](int s, int slot) {  // past the end: the last step again, which is left out
+    const int k0 = (s < t.s1 ? s : t.s1 - 1) * kStep;
 #pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const int row = j * 16 + l16 < nv ? j * 16 + l16 : nv - 1;
-    br[j] = p.b.codes + bskip + (n0 + row) * p.b.ld;
-    ba[j] = p.b.alpha + bskip_s + (n0 + row) * p.b.lds;
-    bs[j] = p.b.scale + bskip_s + (n0 + row) * p.b.lds;
-  }
-  for (int at = tid; at < BM * blocks; at += 64 * kFewWaves) {
-    const int row = at / blocks, b = at - row * blocks;
-    const int64_t from = (m0 + (row < mv ? row : mv - 1)) * p.a.lds + b;
-    lds.r[at] = p.a.scale[from] * __builtin_amdgcn_rcpf(p.a.alpha[from]);
-  }
-  __syncthreads();
-
+    for (int i = 0; i < LOADS; ++i)
+      load_to_lds(from[i], i < BM / 8 ? va : vb, k0, &lds.codes[w][slot][i * 1024]);
+  };
+  const int fa0 = fragment_offset(0, q, l16), fb0 = fragment_offset(BM, q, l16);
+  Codes ca[MT], cb[TN];
+  const auto read = [&](int slot) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) cb[j] = read_codes(lds.codes[w][slot], fb0 + j * 16 * kStep);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) ca[i] = read_codes(lds.codes[w][slot], fa0 + i * 16 * kStep);
+  };
   f32x4 acc[MT][TN];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = w * kFewChunk; s < steps; s += kFewWaves * kFewChunk) {
-    Fragment<F32OUT> fa[kFewChunk][MT], fb[kFewChunk][TN];
-    float rb[kFewChunk][TN];
+  const int blocks = (int)(p.steps >> p.shift);
+
+  for (int c0 = t.s0; c0 < t.s1; c0 += kSplitBlocks << p.shift) {
+    // this wavefront's share of the steps whose scales fit
+    const int c1 = c0 + (kSplitBlocks << p.shift) < t.s1 ? c0 + (kSplitBlocks << p.shift) : t.s1;
+    const int share = (c1 - c0 + kSplitWaves - 1) / kSplitWaves;
+    int s = c0 + w * share;
+    const int e = s + share < c1 ? s + share : c1;
 #pragma unroll
-    for (int u = 0; u < kFewChunk; ++u) {
-      const int su = s + u < steps ? s + u : steps - 1;  // past the end: read again, left out below
+    for (int k = 0; k < ST; ++k) load(s + k, k);
+    const int b0 = c0 >> p.shift;
+    if (c0 != t.s0) __syncthreads();  // the scales before are no longer read
+    f32x4 x[EACH], y[EACH];
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
-        fb[u][j] = load_fragment<F32OUT>(br[j] + (int64_t)su * kStep, q);
+    for (int i = 0; i < EACH; ++i) {
+      const int at = tid + i * NT, row = at / QUADS, k = b0 + at % QUADS * 4;
+      x[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      y[i] = f32x4{1.0f, 1.0f, 1.0f, 1.0f};
+      if (ROWS * QUADS % NT == 0 || row < ROWS) {
+        const bool isa = row < BM;
+        int rr = isa ? row : row - BM;
+        const int last = (isa ? t.mv : t.nv) - 1;
+        rr = rr < last ? rr : last;
+        const int64_t off = (int64_t)rr * (isa ? p.a.lds : p.b.lds) + k;
+        const float *ss = (isa ? t.as : t.bs) + off, *aa = (isa ? t.aa : t.ba) + off;
+        if (k + 4 <= blocks) {
+          x[i] = *(const f32x4u *)ss;
+          y[i] = *(const f32x4u *)aa;
+        } else {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int b = su >> p.shift;
-        rb[u][j] = bs[j][b] * __builtin_amdgcn_rcpf(ba[j][b]);
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        fa[u][i] = load_fragment<F32OUT>(ar[i] + (int64_t)su * kStep, q);
-    }
-#pragma unroll
-    for (int u = 0; u < kFewChunk; ++u) {
-      if (s + u < steps) {
-        const int b = (s + u) >> p.shift;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          float ra[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ra[k] = lds.r[(i * 16 + 4 * q + k) * blocks + b];
-#pragma unroll
-          for (int j = 0; j < TN; ++j) {
-            const f32x4 part = mfma_one(fa[u][i], fb[u][j]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              acc[i][j][k] = fmaf(part[k], ra[k] * rb[u][j], acc[i][j][k]);
-          }
+          for (int u = 0; u < 3; ++u)
+            if (k + u < blocks) {
+              x[i][u] = ss[u];
+              y[i][u] = aa[u];
+            }
         }
       }
+    }
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const int at = tid + i * NT, row = at / QUADS, k = at % QUADS * 4;
+      if (ROWS * QUADS % NT == 0 || row < ROWS)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) lds.r[k + u][row] = x[i][u] * __builtin_amdgcn_rcpf(y[i][u]);
+    }
+    __syncthreads();
+    const auto multiply = [&](const Codes (&xa)[MT], const Codes (&xb)[TN], int step, int i0,
+                              int i1) {
+      const float *r = lds.r[(step >> p.shift) - b0];
+      Fragment<F32OUT> fb[TN];
+      f32x4 rb[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        fb[j] = make_fragment<F32OUT>(xb[j].lo, xb[j].hi);
+        rb[j] = *(const f32x4 *)&r[BM + j * 16 + 4 * q];
+      }
+#pragma unroll
+      for (int i = i0; i < i1; ++i) {
+        const Fragment<F32OUT> fa = make_fragment<F32OUT>(xa[i].lo, xa[i].hi);
+        const float ra = r[i * 16 + l16];
+        f32x4 part[TN];
+        mfma_row(part, fb, fa);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            acc[i][j][k] = fmaf(part[j][k], ra * rb[j][k], acc[i][j][k]);
+      }
+    };
+    if constexpr (ST == 1) {
+      wait_loads();
+      read(0);
+      for (; s < e; ++s) {
+        Codes xa[MT], xb[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) xb[j] = cb[j];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) xa[i] = ca[i];
+        wait_lds();
+        load(s + 1, 0);
+        multiply(xa, xb, s, 0, MT);
+        wait_loads();
+        read(0);
+      }
+      wait_lds();
+    } else {
+      int slot = 0;
+      for (; s < e; ++s) {
+        wait_loads<(ST - 1) * LOADS>();
+        read(slot);
+        wait_lds();
+        load(s + ST, slot);
+        multiply(ca, cb, s, 0, MT);
+        slot = slot + 1 < ST ? slot + 1 : 0;
+      }
+      wait_loads();
     }
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) lds.sum[w][i * TN + j][4 * q + k][l16] = acc[i][j][k];
+    for (int j = 0; j < TN; ++j) lds.sum[w][i * TN + j][lane] = acc[i][j];
   __syncthreads();
-  for (int at = tid; at < BM * BN; at += 64 * kFewWaves) {
-    const int m = at / BN, n = at % BN;
-    if (m < mv && n < nv) {
-      float v = 0.0f;
+  for (int at = w; at < MT * TN; at += kSplitWaves) {
+    f32x4 v = lds.sum[0][at][lane];
 #pragma unroll
-      for (int k = 0; k < kFewWaves; ++k) v += lds.sum[k][m / 16 * TN + n / 16][m % 16][n % 16];
-      const int64_t to = (m0 + m) * p.ldc + n0 + n;
-      if constexpr (F32OUT)
-        ((float *)p.out)[to] = v;
-      else
-        ((__bf16 *)p.out)[to] = (__bf16)v;
+    for (int k = 1; k < kSplitWaves; ++k) {
+      const f32x4 o = lds.sum[k][at][lane];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] += o[c];
     }
+    const int row = at / TN * 16 + l16, col = at % TN * 16 + 4 * q;
+    if (row < t.mv) store_values<F32OUT>(t.out, row * p.ldc + col, v, t.nv - col);
   }
 }
 
-template <int MT, int TN, int MODE, bool F32OUT>
-__global__ __launch_bounds__(64 * kFewWaves) void k_matmul_few(ProductArgs p) {
-  matmul_few<MT, TN, MODE, F32OUT>(p);
+template <int MT, int TN, int ST, int MODE, bool F32OUT>
+__global__ __launch_bounds__(64 * kSplitWaves, 2) void k_matmul_split(ProductArgs p) {
+  matmul_split<MT, TN, ST, MODE, F32OUT>(p);
 }
 
 }  // namespace tfp8
@@ -669,37 +828,82 @@ tfp8_status launch_tiles(void (*kernel)(ProductArgs), ProductArgs p, int bm, int
   return launch(kernel, (unsigned)(mt * nt * times), threads, st, p);
 }
 
+// How long a kernel takes for tiles of bm x bn, by what a round of its workgroups took in products of
+// 1024 to 4096 rows and columns and 1024 to 4096 codes deep (ns): `first` and `step` a step where
+// every compute unit has one workgroup, and the same where it has all `slots` that fit.
+struct Pace {
+  int bm, bn, slots;
+  int64_t first, step, first_full, step_full;
+};
+
+int64_t estimate(const Pace &k, int64_t tiles, int64_t steps, int64_t cus) {
+  const int64_t one = k.first + steps * k.step, full = k.first_full + steps * k.step_full;
+  const int64_t round = k.slots * cus, rest = tiles % round;
+  int64_t t = tiles / round * full;
+  if (rest > cus)
+    t += one + (full - one) * (rest - cus) / (round - cus);
+  else if (rest > 0)
+    t += one;
+  return t;
+}
+
 template <int MODE, bool F32OUT>
 tfp8_status launch_product(const ProductArgs &p, hipStream_t st) {
-  const int64_t times = MODE == kGroupedDepth ? p.groups : 1;
-  // rows that share a B: all of them, or an even share of them a group
-  const int64_t together = MODE == kGroupedRows ? (p.m + p.groups - 1) / p.groups : p.m;
-  if constexpr (MODE != kGroupedDepth) {
-    const int64_t blocks = p.steps >> p.shift;
-    if (together <= 16 && 16 * blocks <= kFewScales)
-      return launch_tiles(k_matmul_few<1, 1, MODE, F32OUT>, p, 16, 16, 1, 64 * kFewWaves, st);
-    if (together <= 32 && 32 * blocks <= kFewScales)
-      return launch_tiles(k_matmul_few<2, 2, MODE, F32OUT>, p, 32, 32, 1, 64 * kFewWaves, st);
-  }
-  // Large tiles, one workgroup a compute unit, or small ones, two a unit: slower for the same work,
-  // but with less left over at the edges and in the last round.  Whichever is done sooner, by the
-  // nanoseconds a step of a round took (8192 x 8192 x 8192): 2150 for 256 x 256 and 1470 for 128 x
-  // 128 with bfloat16 outputs, 2050 for 256 x 128 and 2140 with float32 ones; a last round of small
-  // tiles that leaves every unit one at most takes 0.6 of that.
-  const int64_t cus = cu_count();
+  const int64_t times = MODE == kGroupedDepth ? p.groups : 1, cus = cu_count();
   const auto tiles = [&](int bm, int bn) {
     int64_t mt = (p.m + bm - 1) / bm;
     if (MODE == kGroupedRows) mt += p.groups / 2;  // half a tile a group is left over
     return mt * ((p.n + bn - 1) / bn) * times;
   };
-  constexpr int BM = 256, BN = F32OUT ? 128 : 256;
-  const int64_t large = (tiles(BM, BN) + cus - 1) / cus * (F32OUT ? 2050 : 2150);
-  const int64_t small = tiles(128, 128), rest = small % (2 * cus), t = F32OUT ? 2140 : 1470;
-  const int64_t small_ns = small / (2 * cus) * t + (rest > cus ? t : rest ? t * 6 / 10 : 0);
-  if (large < small_ns)
-    return launch_tiles(k_matmul_tile<BM, BN, F32OUT ? 4 : 2, F32OUT ? 2 : 4, MODE, F32OUT>, p, BM,
-                        BN, times, 512, st);
-  return launch_tiles(k_matmul_tile<128, 128, 2, 2, MODE, F32OUT>, p, 128, 128, times, 256, st);
+  if constexpr (MODE != kGroupedDepth) {
+    // Few rows that share a B (an even share of them a group): what counts is how many of B's bytes
+    // are in flight.  One row of 4096 x 4096: 6.4 us with 16 x 16 tiles, four workgroups a
+    // compute unit, 10.6 with 32 x 64; 24 rows of 10240 x 5120: 16.6 us against 15.2.
+    const int64_t together = MODE == kGroupedRows ? (p.m + p.groups - 1) / p.groups : p.m;
+    if (together <= 16 || (together <= 64 && tiles(32, 64) < cus / 4))
+      return launch_tiles(k_matmul_split<1, 1, 1, MODE, F32OUT>, p, 16, 16, times, 512, st);
+    if (together <= 64)
+      return launch_tiles(k_matmul_split<2, 4, 1, MODE, F32OUT>, p, 32, 64, times, 512, st);
+  }
+  // Otherwise the kernel whose rounds are done first: large tiles use the matrix cores best, small
+  // ones leave less over at the edges and in the last round, and a divided depth is for products
+  // with fewer tiles than compute units.
+  constexpr Pace kPace[2][4] = {
+      {{256, 256, 1, 9700, 2060, 9700, 2060},
+       {128, 128, 2, 5000, 850, 7500, 1250},
+       {64, 64, 4, 4200, 445, 7000, 840},
+       {64, 64, 1, 8500, 257, 8500, 257}},
+      {{256, 128, 1, 8600, 2000, 8600, 2000},
+       {128, 128, 2, 7800, 1310, 11000, 2480},
+       {64, 64, 4, 5300, 540, 8500, 1450},
+       {64, 64, 1, 9000, 310, 9000, 310}}};
+  const int64_t steps =
+      MODE == kGroupedDepth ? (p.rows / p.groups + kStep - 1) / kStep : p.steps;
+  int best = 0;
+  int64_t least = 0;
+  for (int i = 0; i < 4; ++i) {
+    const Pace &k = kPace[F32OUT][i];
+    const int64_t ns = estimate(k, tiles(k.bm, k.bn), steps, cus);
+    if (i == 0 || ns < least) {
+      best = i;
+      least = ns;
+    }
+  }
+  const Pace &k = kPace[F32OUT][best];
+  switch (best) {
+    case 0:
+      return launch_tiles(
+          k_matmul_tile<256, F32OUT ? 128 : 256, F32OUT ? 4 : 2, F32OUT ? 2 : 4, 2, 0, MODE, F32OUT>,
+          p, k.bm, k.bn, times, 512, st);
+    case 1:
+      return launch_tiles(k_matmul_tile<128, 128, 2, 4, 2, 0, MODE, F32OUT>, p, k.bm, k.bn, times,
+                          512, st);
+    case 2:
+      return launch_tiles(k_matmul_tile<64, 64, 2, 2, 2, 16, MODE, F32OUT>, p, k.bm, k.bn, times,
+                          256, st);
+    default:
+      return launch_tiles(k_matmul_split<4, 4, 1, MODE, F32OUT>, p, k.bm, k.bn, times, 512, st);
+  }
 }
 
 template <int MODE>
