@@ -13,7 +13,15 @@
 // c read eight rows, the eight c of a row read 8 C consecutive columns (a 128-byte line).  The
 // transform is k_compress's: register stages over the R rows, then the butterfly over the lanes j.
 // It leaves lane j with R consecutive codes of each column, and the eight lanes of a column store its
-// whole block, so nothing passes through LDS.
+// whole block, so no element passes through LDS.  The scales do: a workgroup takes four blocks that
+// follow one another in an output row, and stores a column's four alphas and four scales as 16 bytes
+// each, where single floats would each cost a write of a line.
+//
+// Bound by HBM.  [16384, 5120] bfloat16, B = 128 (257 MB with the scales): 54 us, 4.76 TB/s, where a
+// large copy reaches 4.96; before the scales went out together and whole blocks lost their
+// per-row conditions, 67 us.  [16384, 5120] float32: 92 us, 4.6 TB/s.  Odd rows and columns: 61 us.
+// Half as many columns a lane (six wavefronts a SIMD instead of four) took 60 us; non-temporal
+// loads and stores were 1-2% faster here and 13-17% slower on data that is still in the caches.
 #include <math.h>
 #include <stdint.h>
 
@@ -26,8 +34,10 @@ namespace tfp8 {
 
 // Columns a lane holds: 16 bytes of a row, or as many as 512 bytes of a column leave room for.
 constexpr int transposed_columns(int B, int es) {
-  return 16 / es < 512 / (B / 8 * es) ? 16 / es : 512 / (B / 8 * es);
+  const int most = 512 / (B / 8 * es);
+  return 16 / es < most ? 16 / es : most;
 }
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 struct TransposeArgs {
   const void *x;
@@ -35,7 +45,7 @@ struct TransposeArgs {
   const int64_t *offsets;  // NULL: one group
   int groups;
   int64_t blocks;  // blocks of an output row
-  int64_t tiles;   // column tiles
+  uint32_t tiles;  // column tiles
   float TBB, sqrtTB, sqrtTBB, invC;
   uint8_t *codes;
   float *alpha, *scale;
@@ -69,7 +79,7 @@ __device__ __forceinline__ void column_scales(float (&v)[R], float M, float SS,
   }
 }
 
-template <int B, bool F32IN, bool ROT, bool WIDE>
+template <int B, bool F32IN, bool ROT>
 __global__ __launch_bounds__(256) void k_compress_t(TransposeArgs p) {
   constexpr int ES = F32IN ? 4 : 2;
   constexpr int R = B / 8;
@@ -77,49 +87,58 @@ __global__ __launch_bounds__(256) void k_compress_t(TransposeArgs p) {
   constexpr int DW = C * ES / 4;  // dwords a lane holds of a row
   const int lane = threadIdx.x & 63;
   const int j = lane & 7, c = lane >> 3;
-  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t kb = wave / p.tiles, ct = wave % p.tiles;
-  if (kb >= p.blocks) return;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ float scales[2][8 * C][4];
+  // the launch's tiles in eight contiguous parts, one for each XCD, columns first
+  const uint32_t per = gridDim.x >> 3, over = gridDim.x & 7, x8 = blockIdx.x & 7;
+  const uint32_t bid = x8 * per + (x8 < over ? x8 : over) + (blockIdx.x >> 3);
+  const int64_t kb0 = (int64_t)(bid / p.tiles) * 4, kb = kb0 + w;
+  const int64_t ct = bid % p.tiles;
 
-  int64_t row0;
-  int rows;
-  if (p.offsets) {
-    const GroupTile g = tile_of_groups(p.offsets, p.groups, p.rows, B, kb, p.groups - 1);
-    row0 = g.row0;
-    rows = g.rows;
-  } else {
-    row0 = kb * B;
-    rows = (int)(p.rows - row0 < B ? p.rows - row0 : B);
+  int64_t row0 = 0;
+  int rows = 0;
+  if (kb < p.blocks) {
+    if (p.offsets) {
+      const GroupTile g = tile_of_groups(p.offsets, p.groups, p.rows, B, kb, p.groups - 1);
+      row0 = g.row0;
+      rows = g.rows;
+    } else {
+      row0 = kb * B;
+      rows = (int)(p.rows - row0 < B ? p.rows - row0 : B);
+    }
   }
   const int64_t col0 = (ct * 8 + c) * C;
   const int cols = (int)(p.cols - col0 < C ? p.cols - col0 : C);
 
+  // this lane's rows and columns; a whole block of whole chunks takes the loads without conditions
   uint32_t d[R][DW];
+  const char *at = (const char *)p.x + ((row0 + R * j) * p.ldx + col0) * ES;
+  const int64_t next = p.ldx * ES;
+  typedef uint32_t chunk_t __attribute__((ext_vector_type(DW), aligned(ES)));  // at any element
+  if (rows == B && __all(cols == C)) {
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int row = R * j + i;
+    for (int i = 0; i < R; ++i) {
+      const chunk_t t = *(const chunk_t *)(at + i * next);
 #pragma unroll
-    for (int k = 0; k < DW; ++k) d[i][k] = 0;
-    if (row < rows) {
-      const char *at = (const char *)p.x + ((row0 + row) * p.ldx + col0) * ES;
-      if (WIDE && cols == C) {
-        if constexpr (DW == 4) {
-          const u32x4 t = *(const u32x4 *)at;
+      for (int k = 0; k < DW; ++k) d[i][k] = t[k];
+    }
+  } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) d[i][k] = t[k];
-        } else {
-          const u32x2 t = *(const u32x2 *)at;
-          d[i][0] = t[0];
-          d[i][1] = t[1];
-        }
-      } else {
+    for (int i = 0; i < R; ++i) {
 #pragma unroll
-        for (int k = 0; k < C; ++k)
+      for (int k = 0; k < DW; ++k) d[i][k] = 0;
+      if (R * j + i < rows && cols == C) {
+        const chunk_t t = *(const chunk_t *)(at + i * next);
+#pragma unroll
+        for (int k = 0; k < DW; ++k) d[i][k] = t[k];
+      } else if (R * j + i < rows) {
+#pragma unroll
+        for (int k = 0; k < C - 1; ++k)
           if (k < cols) {
             if constexpr (F32IN)
-              d[i][k] = ((const uint32_t *)at)[k];
+              d[i][k] = ((const uint32_t *)(at + i * next))[k];
             else
-              d[i][k / 2] |= (uint32_t)((const uint16_t *)at)[k] << (16 * (k & 1));
+              d[i][k / 2] |= (uint32_t)((const uint16_t *)(at + i * next))[k] << (16 * (k & 1));
           }
       }
     }
@@ -149,7 +168,7 @@ __global__ __launch_bounds__(256) void k_compress_t(TransposeArgs p) {
     float cm, alpha, s;
     column_scales<R>(v, M, SS, p, cm, alpha, s);
     cm *= sj;
-    if (k < cols) {
+    if (k < cols && kb < p.blocks) {
       const int64_t o = (col0 + k) * p.blocks + kb;
       uint8_t *to = p.codes + o * B + R * pj;
 #pragma unroll
@@ -161,10 +180,24 @@ __global__ __launch_bounds__(256) void k_compress_t(TransposeArgs p) {
                             fmaf(v[i + 4 * t + 2], cm, 0.0f), fmaf(v[i + 4 * t + 3], cm, 0.0f));
         *(u32x4 *)(to + i) = q;
       }
-      if (j == 0) {
-        p.alpha[o] = alpha;
-        p.scale[o] = s;
-      }
+    }
+    if (j == 0) {
+      scales[0][c * C + k][w] = alpha;
+      scales[1][c * C + k][w] = s;
+    }
+  }
+  // the scales of a column's four blocks together
+  __syncthreads();
+  for (int t = threadIdx.x; t < 16 * C; t += 256) {
+    const int which = t / (8 * C), i = t % (8 * C);
+    const int64_t col = ct * 8 * C + i;
+    if (col < p.cols) {
+      float *to = (which ? p.scale : p.alpha) + col * p.blocks + kb0;
+      const float *from = scales[which][i];
+      if (kb0 + 4 <= p.blocks)
+        *(f32x4_any *)to = f32x4_any{from[0], from[1], from[2], from[3]};
+      else
+        for (int k = 0; kb0 + k < p.blocks; ++k) to[k] = from[k];
     }
   }
 }
@@ -179,13 +212,10 @@ template <int B, bool F32, bool ROT>
 tfp8_status launch_compress_t(TransposeArgs p, hipStream_t st) {
   constexpr int ES = F32 ? 4 : 2;
   constexpr int C = transposed_columns(B, ES);
-  p.tiles = (p.cols + 8 * C - 1) / (8 * C);
-  const int64_t grid = (p.tiles * p.blocks + 3) / 4;
+  const int64_t tiles = (p.cols + 8 * C - 1) / (8 * C), grid = tiles * ((p.blocks + 3) / 4);
+  p.tiles = (uint32_t)tiles;
   if (grid > ((int64_t)1 << 24) - 1) return TFP8_E_SIZE;
-  // whole-vector loads need every row of a column chunk aligned to the vector
-  const bool wide = aligned(p.x, C * ES) && (p.ldx * ES) % (C * ES) == 0;
-  return wide ? launch(k_compress_t<B, F32, ROT, true>, (unsigned)grid, 256, st, p)
-              : launch(k_compress_t<B, F32, ROT, false>, (unsigned)grid, 256, st, p);
+  return launch(k_compress_t<B, F32, ROT>, (unsigned)grid, 256, st, p);
 }
 
 }  // namespace

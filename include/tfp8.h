@@ -206,9 +206,8 @@ int64_t tfp8_padded_rows(int64_t rows, int32_t groups, int32_t block);
  * runs over the rows.  Rows past the end of a group's last block count as zeros; blocks past the
  * last group's are written as zero blocks.  offsets = NULL with groups = 1: all rows are one group.
  * Rows past offsets[groups] are left out.  flags: 0 or TFP8_FLAG_NO_ROTATION (TFP8_E_ARG: no
- * product takes INT8 codes).  x is aligned to its elements; any ldx is accepted, and rows that
- * are aligned to 16 bytes are read faster.  rows * ldx and cols * kp are at most TFP8_MAX_N
- * (TFP8_E_SIZE). */
+ * product takes INT8 codes).  x is aligned to its elements; rows may start at any of them.
+ * rows * ldx and cols * kp are at most TFP8_MAX_N (TFP8_E_SIZE). */
 tfp8_status tfp8_compress_t(const void *x, tfp8_dtype x_dtype, int64_t rows, int64_t cols,
                             int64_t ldx, const int64_t *offsets, int32_t groups, int32_t block,
                             float target, uint32_t flags, uint8_t *codes, float *alpha,
