@@ -291,15 +291,17 @@ __device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
 }
 
 // LDS of a tile: NS stages of a step's codes, A's rows then B's, and scales r: those of a step for
-// each stage, or (CHUNK > 0) those of CHUNK blocks.
-template <int BM_, int BN_, int NS_, int CHUNK_>
+// each stage, or (CHUNK > 0) those of CHUNK blocks.  KS > 1: the workgroup's wavefronts form KS teams
+// with stages of their own, and team g takes steps g, g + KS, ...
+template <int BM_, int BN_, int NS_, int KS_, int CHUNK_>
 struct Stages {
-  static constexpr int BM = BM_, BN = BN_, NS = NS_, CHUNK = CHUNK_;
-  alignas(1024) uint8_t codes[NS][(BM + BN) * kStep];
+  static constexpr int BM = BM_, BN = BN_, NS = NS_, KS = KS_, CHUNK = CHUNK_;
+  static_assert(KS == 1 || CHUNK > 0, "teams share the scales of a chunk");
+  alignas(1024) uint8_t codes[KS][NS][(BM + BN) * kStep];
   float r[CHUNK ? CHUNK : NS][BM + BN];
 };
 
-// Filling the stages.
+// Filling the stages of one team of NW wavefronts.
 template <class STAGES, int NW>
 struct Feed {
   static constexpr int BM = STAGES::BM, BN = STAGES::BN, CHUNK = STAGES::CHUNK;
@@ -310,7 +312,7 @@ struct Feed {
   static_assert(BM % 64 == 0 && ROWS % 64 == 0, "a wavefront's scales are of one operand");
 
   STAGES &lds;
-  int w, shift, first, blocks;
+  int team, w, shift, first, blocks;  // w: the wavefront within its team
   i32x4 ra[LA], rb[LB];
   int va, vb;
   const char *sp[SC], *ap[SC];  // a wavefront's rows are of one operand
@@ -323,8 +325,10 @@ struct Feed {
   // to the operand's end, past which rows read as zeros.
   __device__ __forceinline__ Feed(STAGES &l, const ProductArgs &p, const Job &t)
       : lds(l), shift(p.shift) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = threadIdx.x & 63;
+    team = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / NW;
+    w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % NW;
+    const int tid = w * 64 + lane;
     const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
     va = (lane >> 3) * (int)p.a.ld + chunk;
     vb = (lane >> 3) * (int)p.b.ld + chunk;
@@ -359,22 +363,22 @@ struct Feed {
     for (int i = 0; i < LA + LB; ++i) {
       if (i * parts / (LA + LB) != part) continue;
       if (i < LA)
-        load_to_lds(ra[i], va, s * kStep, &lds.codes[stage][(i * NW + w) * 1024]);
+        load_to_lds(ra[i], va, s * kStep, &lds.codes[team][stage][(i * NW + w) * 1024]);
       else
         load_to_lds(rb[i - LA], vb, s * kStep,
-                    &lds.codes[stage][BM * kStep + ((i - LA) * NW + w) * 1024]);
+                    &lds.codes[team][stage][BM * kStep + ((i - LA) * NW + w) * 1024]);
     }
   }
   // Scales, r = scale / alpha of every row (A's, then B's).
   //
   // CHUNK > 0: the next CHUNK blocks' at once, from block b on, four to a thread.
   __device__ __forceinline__ void fill_scales(int b, const ProductArgs &p, const Job &t) {
-    constexpr int QUADS = CHUNK / 4, EACH = ROWS * QUADS / NT;
-    static_assert(CHUNK % 4 == 0 && ROWS * QUADS % NT == 0, "whole quads for every thread");
+    constexpr int QUADS = CHUNK / 4, ALL = NT * STAGES::KS, EACH = ROWS * QUADS / ALL;
+    static_assert(CHUNK % 4 == 0 && ROWS * QUADS % ALL == 0, "whole quads for every thread");
     f32x4 x[EACH], y[EACH];
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
-      const int at = (int)threadIdx.x + i * NT, row = at / QUADS, k = b + at % QUADS * 4;
+      const int at = (int)threadIdx.x + i * ALL, row = at / QUADS, k = b + at % QUADS * 4;
       const bool isa = row < BM;
       int rr = isa ? row : row - BM;
       const int last = (isa ? t.mv : t.nv) - 1;
@@ -397,7 +401,7 @@ struct Feed {
     }
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
-      const int at = (int)threadIdx.x + i * NT, row = at / QUADS, k = at % QUADS * 4;
+      const int at = (int)threadIdx.x + i * ALL, row = at / QUADS, k = at % QUADS * 4;
 #pragma unroll
       for (int u = 0; u < 4; ++u) lds.r[k + u][row] = x[i][u] * __builtin_amdgcn_rcpf(y[i][u]);
     }
@@ -457,31 +461,35 @@ template <int TM, int TN, bool WIDE, class STAGES, class FEED>
 __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const ProductArgs &p,
                                           const Job &job, int mrow, int nrow,
                                           f32x4 (&acc)[TM][TN]) {
-  constexpr int NS = STAGES::NS, BM = STAGES::BM, CHUNK = STAGES::CHUNK;
+  constexpr int NS = STAGES::NS, KS = STAGES::KS, BM = STAGES::BM, CHUNK = STAGES::CHUNK;
+  constexpr bool STEADY = NS > 2 || KS > 1;
   constexpr int NP = TM >= 8 ? 3 : TM >= 3 ? 2 : 1;  // a step's loads go out in this many shares
   constexpr int LOADS = FEED::LA + FEED::LB;
   const int s0 = job.s0, s1 = job.s1;
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
   const int fa0 = fragment_offset(mrow, q, l16), fb0 = fragment_offset(BM + nrow, q, l16);
-  int s = s0;
+  const int team = KS > 1 ? feed.team : 0;
+  const auto &codes = lds.codes[team];
+  int s = s0 + team;
   int chunk0 = s0 >> p.shift;  // first block of the scales in LDS (CHUNK)
-  // With more than two stages every step issues its loads, past the end those of the last step
-  // again, so that the number in flight is always the same.
+  // With more than two stages, or teams, every step issues its loads, past the end those of the last
+  // step again, so that the number in flight is always the same, and a team that is a step short
+  // works on codes (with its scales taken as zero).
   const auto load = [&](int x, int slot, int part, int parts) {
-    if (NS > 2)
+    if (STEADY)
       feed.load_step(x < s1 ? x : s1 - 1, slot, part, parts);
     else if (x < s1)
       feed.load_step(x, slot, part, parts);
   };
   feed.load_scales(s);
 #pragma unroll
-  for (int k = 0; k < NS - 1; ++k) load(s + k, k, 0, 1);
+  for (int k = 0; k < NS - 1; ++k) load(s + k * KS, k, 0, 1);
   if (NS == 2) wait_loads();
   feed.put_scales(s, 0);
   if constexpr (CHUNK > 0) feed.fill_scales(chunk0, p, job);
   wait_loads<(NS - 2) * LOADS>();
   lds_barrier();
-  load(s + NS - 1, NS - 1, 0, NP);
+  load(s + (NS - 1) * KS, NS - 1, 0, NP);
   if (NP == 1 && s + 1 < s1) feed.load_scales(s + 1);
   // where the scales of step x, in slot y, are
   const auto scales = [&](int x, int y) {
@@ -492,11 +500,11 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
   float ra, rprev = 0.0f;  // A's scales of this row of tiles and of the one before
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
-    fb[j] = read_fragment<WIDE>(lds.codes[0], fb0 + j * 16 * kStep);
+    fb[j] = read_fragment<WIDE>(codes[0], fb0 + j * 16 * kStep);
     rb[j] = part[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  fa = read_fragment<WIDE>(lds.codes[0], fa0);
-  ra = scales(s, 0)[mrow + l16];
+  fa = read_fragment<WIDE>(codes[0], fa0);
+  ra = KS == 1 || s < s1 ? scales(s, 0)[mrow + l16] : 0.0f;
   // part[j] of the row of tiles before, scaled and added
   auto add_part = [&](f32x4 (&to)[TN], int j) {
 #pragma unroll
@@ -506,7 +514,7 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
     asm volatile("" : "+v"(to[j]));
   };
   const auto next = [](int slot) { return NS == 2 ? slot ^ 1 : slot + 1 < NS ? slot + 1 : 0; };
-  for (int slot = 0; s < s1; ++s, slot = next(slot)) {
+  for (int slot = 0; s - team < s1; s += KS, slot = next(slot)) {
     const int ahead = next(slot);
     const int back = NS == 2 ? ahead : slot ? slot - 1 : NS - 1;  // of the step NS - 1 ahead
 #pragma unroll
@@ -516,23 +524,25 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
         wait_loads<(NS - 2) * LOADS>();
         if (s + 1 < s1) feed.put_scales(s + 1, ahead);
         lds_barrier();
-        load(s + NS, slot, 0, NP);
+        load(s + NS * KS, slot, 0, NP);
         if (NP == 1 && s + 2 < s1) feed.load_scales(s + 2);
         if constexpr (CHUNK > 0) {
-          if (s + 1 < s1 && ((s + 1) >> p.shift) - chunk0 == CHUNK) {
-            chunk0 += CHUNK;
+          const int n0 = s - team + KS, n1 = n0 + KS - 1;  // the teams' next steps
+          if (n0 < s1 && (n1 >> p.shift) - chunk0 >= CHUNK) {
+            chunk0 = n0 >> p.shift;
             feed.fill_scales(chunk0, p, job);
             lds_barrier();
           }
         }
       } else if (i + 1 < NP) {
-        load(s + NS - 1, back, i + 1, NP);
+        load(s + (NS - 1) * KS, back, i + 1, NP);
         if (i + 2 == NP && s + 1 < s1) feed.load_scales(s + 1);
       }
       const int ns = last ? ahead : slot;
       const int ni = last ? 0 : i + 1;
-      const Fragment<WIDE> fn = read_fragment<WIDE>(lds.codes[ns], fa0 + ni * 16 * kStep);
-      const float rn = scales(last ? s + 1 : s, ns)[mrow + ni * 16 + l16];
+      const Fragment<WIDE> fn = read_fragment<WIDE>(codes[ns], fa0 + ni * 16 * kStep);
+      const int sn = last ? s + KS : s;
+      const float rn = KS == 1 || sn < s1 ? scales(sn, ns)[mrow + ni * 16 + l16] : 0.0f;
       // B's scales of this step replace the last one's once its last row is added
       auto next_scales = [&](int j) {
         if (i == 0) rb[j] = *(const f32x4 *)&scales(s, slot)[BM + nrow + j * 16 + 4 * q];
@@ -546,14 +556,14 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
         mfma_row(part, fb, fa);
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-          if (last) fb[j] = read_fragment<WIDE>(lds.codes[ns], fb0 + j * 16 * kStep);
+          if (last) fb[j] = read_fragment<WIDE>(codes[ns], fb0 + j * 16 * kStep);
       } else {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
           add_part(acc[i ? i - 1 : TM - 1], j);
           next_scales(j);
           part[j] = mfma_codes(fb[j], fa);
-          if (last) fb[j] = read_fragment<WIDE>(lds.codes[ns], fb0 + j * 16 * kStep);
+          if (last) fb[j] = read_fragment<WIDE>(codes[ns], fb0 + j * 16 * kStep);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -564,20 +574,21 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
   }
 #pragma unroll
   for (int j = 0; j < TN; ++j) add_part(acc[TM - 1], j);
-  if (NS > 2) wait_loads();  // no load may arrive after the workgroup has given its LDS back
+  if (STEADY) wait_loads();  // no load may arrive after the workgroup has given its LDS back
 }
 
 // The kernel only calls this function: a kernel's own body is also read by the host's pass, which
 // does not know these builtins.
-template <int BM, int BN, int WM, int WN, int NS, int CHUNK, int MODE, bool F32OUT>
+template <int BM, int BN, int WM, int WN, int NS, int KS, int CHUNK, int MODE, bool F32OUT>
 __device__ __forceinline__ void matmul_tile(const ProductArgs &p) {
-  constexpr int TM = BM / 16 / WM, TN = BN / 16 / WN;
-  using STAGES = Stages<BM, BN, NS, CHUNK>;
+  constexpr int TM = BM / 16 / WM, TN = BN / 16 / WN, KEEP = TM / KS;
+  using STAGES = Stages<BM, BN, NS, KS, CHUNK>;
   __shared__ STAGES lds;
   Job t;
   if (!find_job<BM, BN, MODE, F32OUT ? 4 : 2>(p, t)) return;
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = all % (WM * WN), team = all / (WM * WN);
   const int mrow = w / WN * TM * 16, nrow = w % WN * TN * 16;
   f32x4 acc[TM][TN];
 #pragma unroll
@@ -588,36 +599,64 @@ __device__ __forceinline__ void matmul_tile(const ProductArgs &p) {
     Feed<STAGES, WM * WN> feed(lds, p, t);
     run_steps<TM, TN, F32OUT>(lds, feed, p, t, mrow, nrow, acc);
   }
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
+  // row of tiles i of this wavefront
+  const auto store_row = [&](int i, const f32x4 (&v)[TN]) {
     const int row = mrow + i * 16 + l16;
     if constexpr (F32OUT) {
       if (row < t.mv) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
           const int col = nrow + j * 16 + 4 * q;
-          store_values<true>(t.out, row * p.ldc + col, acc[i][j], t.nv - col);
+          store_values<true>(t.out, row * p.ldc + col, v[j], t.nv - col);
         }
       }
     } else {
 #pragma unroll
       for (int j = 0; j < TN; j += 2) {  // every lane takes part in the swaps
         const int col = nrow + j * 16;
-        store_pair(t.out, row * p.ldc + col, q, acc[i][j], acc[i][j + 1],
-                   row < t.mv ? t.nv - col : 0);
+        store_pair(t.out, row * p.ldc + col, q, v[j], v[j + 1], row < t.mv ? t.nv - col : 0);
       }
+    }
+  };
+  if constexpr (KS == 1) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) store_row(i, acc[i]);
+  } else {
+    // two teams: each stores half of its rows of tiles, and gives the other half to its counterpart
+    static_assert(KS == 2 && sizeof(lds.codes) >= 2 * WM * WN * KEEP * TN * 1024, "teams' sums");
+    f32x4 *sum = (f32x4 *)&lds.codes[0][0][0] + lane;
+    const auto at = [&](int to, int i, int j) {
+      return (((to * WM * WN + w) * KEEP + i) * TN + j) * 64;
+    };
+    lds_barrier();  // both teams' loads have arrived, and their fragments are in registers
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        sum[at(team ^ 1, i, j)] = team == 0 ? acc[i + KEEP][j] : acc[i][j];
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) {
+      f32x4 v[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const f32x4 o = sum[at(team, i, j)];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[j][k] = (team == 0 ? acc[i][j][k] : acc[i + KEEP][j][k]) + o[k];
+      }
+      store_row(team * KEEP + i, v);
     }
   }
 }
 
-template <int BM, int BN, int WM, int WN, int NS, int CHUNK, int MODE, bool F32OUT>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_matmul_tile(ProductArgs p) {
-  matmul_tile<BM, BN, WM, WN, NS, CHUNK, MODE, F32OUT>(p);
+template <int BM, int BN, int WM, int WN, int NS, int KS, int CHUNK, int MODE, bool F32OUT>
+__global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_matmul_tile(ProductArgs p) {
+  matmul_tile<BM, BN, WM, WN, NS, KS, CHUNK, MODE, F32OUT>(p);
 }
 
 // --------------------------------------------------------------------------------------------
-// Products too small to fill the chip with tiles whose wavefronts share them: few rows (decoding,
-// where B's bytes bound the product) or few tiles.  A workgroup takes one tile of 16 MT rows of A
+// Few rows (decoding): B's bytes bound the product.  A workgroup takes one tile of 16 MT rows of A
 // (its group's) by 16 TN of B, and its eight wavefronts divide the depth: each computes the whole tile
 // over its share of the steps, and the eight are added up through LDS in a fixed order at the end.
 // Each wavefront has ST stages of LDS to itself, so there is no barrier in the loop: it waits for
@@ -866,23 +905,27 @@ tfp8_status launch_product(const ProductArgs &p, hipStream_t st) {
       return launch_tiles(k_matmul_split<2, 4, 1, MODE, F32OUT>, p, 32, 64, times, 512, st);
   }
   // Otherwise the kernel whose rounds are done first: large tiles use the matrix cores best, small
-  // ones leave less over at the edges and in the last round, and a divided depth is for products
-  // with fewer tiles than compute units.
-  constexpr Pace kPace[2][4] = {
+  // ones leave less over at the edges and in the last round, and two teams halve the steps of a
+  // product with about as many tiles as compute units.
+  constexpr int kKinds = 5;
+  constexpr Pace kPace[2][kKinds] = {
       {{256, 256, 1, 9700, 2060, 9700, 2060},
-       {128, 128, 2, 5000, 850, 7500, 1250},
-       {64, 64, 4, 4200, 445, 7000, 840},
-       {64, 64, 1, 8500, 257, 8500, 257}},
+       {128, 128, 2, 5000, 840, 7500, 1300},
+       {128, 128, 1, 8000, 620, 8000, 620},  // two teams
+       {64, 64, 4, 4200, 460, 6200, 900},
+       {64, 64, 2, 4500, 334, 6250, 448}},   // two teams
       {{256, 128, 1, 8600, 2000, 8600, 2000},
-       {128, 128, 2, 7800, 1310, 11000, 2480},
-       {64, 64, 4, 5300, 540, 8500, 1450},
-       {64, 64, 1, 9000, 310, 9000, 310}}};
+       {0, 0, 0, 0, 0, 0, 0},
+       {128, 128, 1, 8800, 1087, 8800, 1087},
+       {64, 64, 4, 5300, 570, 8500, 1440},
+       {64, 64, 2, 5300, 433, 9000, 813}}};
   const int64_t steps =
       MODE == kGroupedDepth ? (p.rows / p.groups + kStep - 1) / kStep : p.steps;
   int best = 0;
   int64_t least = 0;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kKinds; ++i) {
     const Pace &k = kPace[F32OUT][i];
+    if (k.slots == 0) continue;  // no sizes at which 128 x 128 without teams would be first
     const int64_t ns = estimate(k, tiles(k.bm, k.bn), steps, cus);
     if (i == 0 || ns < least) {
       best = i;
@@ -890,20 +933,18 @@ tfp8_status launch_product(const ProductArgs &p, hipStream_t st) {
     }
   }
   const Pace &k = kPace[F32OUT][best];
-  switch (best) {
-    case 0:
-      return launch_tiles(
-          k_matmul_tile<256, F32OUT ? 128 : 256, F32OUT ? 4 : 2, F32OUT ? 2 : 4, 2, 0, MODE, F32OUT>,
-          p, k.bm, k.bn, times, 512, st);
-    case 1:
-      return launch_tiles(k_matmul_tile<128, 128, 2, 4, 2, 0, MODE, F32OUT>, p, k.bm, k.bn, times,
-                          512, st);
-    case 2:
-      return launch_tiles(k_matmul_tile<64, 64, 2, 2, 2, 16, MODE, F32OUT>, p, k.bm, k.bn, times,
-                          256, st);
-    default:
-      return launch_tiles(k_matmul_split<4, 4, 1, MODE, F32OUT>, p, k.bm, k.bn, times, 512, st);
-  }
+  const auto run = [&](void (*kernel)(ProductArgs), int threads) {
+    return launch_tiles(kernel, p, k.bm, k.bn, times, threads, st);
+  };
+  if (best == 0)
+    return run(k_matmul_tile<256, F32OUT ? 128 : 256, F32OUT ? 4 : 2, F32OUT ? 2 : 4, 2, 1, 0, MODE,
+                             F32OUT>,
+               512);
+  if constexpr (!F32OUT)
+    if (best == 1) return run(k_matmul_tile<128, 128, 2, 4, 2, 1, 0, MODE, F32OUT>, 512);
+  if (best == 2) return run(k_matmul_tile<128, 128, 2, 2, 2, 2, 16, MODE, F32OUT>, 512);
+  if (best == 3) return run(k_matmul_tile<64, 64, 2, 2, 2, 1, 16, MODE, F32OUT>, 256);
+  return run(k_matmul_tile<64, 64, 2, 2, 2, 2, 16, MODE, F32OUT>, 512);
 }
 
 template <int MODE>
