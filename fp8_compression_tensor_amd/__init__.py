@@ -429,17 +429,17 @@ def _operand(t, block: int, dims: int, name: str):
     [groups, rows, k]; alpha and scale are float32 with k / block values a row, [rows, k / block]
     with contiguous rows, or contiguous in any shape (as compress returns them)."""
     codes, alpha, scale = t
-    # the common form, all contiguous, in the order of what costs least; whatever fails here is
-    # looked at again below
+    # the common form, all contiguous; whatever fails here is looked at again below
     if (isinstance(codes, torch.Tensor) and isinstance(alpha, torch.Tensor)
-            and isinstance(scale, torch.Tensor) and codes.dim() == dims and codes.dtype == torch.uint8 and codes.is_contiguous()
-            and alpha.dtype == scale.dtype == torch.float32 and alpha.is_contiguous()
-            and scale.is_contiguous()
+            and isinstance(scale, torch.Tensor) and codes.dtype is torch.uint8
+            and alpha.dtype is torch.float32 and scale.dtype is torch.float32
+            and codes.is_contiguous() and alpha.is_contiguous() and scale.is_contiguous()
             and codes.get_device() == alpha.get_device() == scale.get_device() >= 0):
-        k, n = codes.shape[-1], codes.numel()
-        if k % block == 0 and alpha.numel() == scale.numel() == n // block:
-            nb = k // block
-            return codes.shape, (codes.data_ptr(), k, alpha.data_ptr(), scale.data_ptr(), nb)
+        shape = codes.shape
+        if len(shape) == dims:
+            k = shape[-1]
+            if k % block == 0 and alpha.numel() == scale.numel() == codes.numel() // block:
+                return shape, (codes.data_ptr(), k, alpha.data_ptr(), scale.data_ptr(), k // block)
     for x, dt, what in ((codes, torch.uint8, "codes"), (alpha, torch.float32, "alpha"),
                         (scale, torch.float32, "scale")):
         if not (isinstance(x, torch.Tensor) and x.is_cuda):
@@ -478,9 +478,9 @@ def _operand(t, block: int, dims: int, name: str):
 
 def _product_out(out, shape, dtype: torch.dtype, a, b):
     """The output, new or checked, of a product of a and b, whose devices are compared."""
+    if a[0].get_device() != b[0].get_device():
+        raise ValueError(f"tensors on different devices ({a[0].device} and {b[0].device})")
     device = a[0].device
-    if device != b[0].device:
-        raise ValueError(f"tensors on different devices ({device} and {b[0].device})")
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not (isinstance(out, torch.Tensor) and out.is_cuda):

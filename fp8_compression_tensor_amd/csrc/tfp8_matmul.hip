@@ -26,28 +26,26 @@ typedef const __attribute__((address_space(3))) void lds_const;
 
 constexpr int kStep = 128;  // contraction depth of one matrix instruction
 
-// A compressed operand: rows of codes `ld` bytes apart, rows of scales `lds` floats apart, and for
-// a stack of them (experts) the distance from one to the next.
+// A compressed operand: rows of codes `ld` bytes apart, rows of scales `lds` floats apart.
 struct Operand {
   const uint8_t *codes;
   const float *alpha, *scale;
-  int64_t ld, lds;
-  int64_t next, next_s;
+  int32_t ld, lds;
 };
 
 enum : int { kDense = 0, kGroupedRows = 1, kGroupedDepth = 2 };
 
+// Kept small: a launch copies it (16 bytes of arguments take 2.6 us to launch, 208 take 3.5).
 struct ProductArgs {
-  Operand a, b;
-  int64_t m, n;          // rows of A (all groups together, kGroupedRows) and of B
-  int64_t steps;         // kStep-deep steps along a row
-  int shift;             // log2(block / kStep): steps 2^shift s .. share a scale
+  Operand a, b;            // kGroupedRows: one b after the other
   const int64_t *offsets;
-  int groups;
-  int64_t rows;          // kGroupedDepth: rows of the uncompressed operands
-  void *out;
-  int64_t ldc, next_c;
-  int mtiles, ntiles;
+  void *out;               // kGroupedDepth: one [m][n] after the other
+  int64_t ldc;
+  int32_t m, n;            // rows of A (all groups together, kGroupedRows) and of B
+  int32_t rows, groups;    // rows: of the uncompressed operands (kGroupedDepth)
+  int32_t steps;           // kStep-deep steps along a row
+  int32_t shift;           // log2(block / kStep): so many steps share a scale
+  int32_t mtiles, ntiles;
 };
 
 // 16 x 16 partial tile over 128 codes: D[4 q + i][l & 15], q = l >> 4, of rows of x by rows of y.
@@ -254,7 +252,7 @@ __device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
     s1 = (g.unit0 + g.units) << p.shift;
     s1 = s1 < p.steps ? s1 : p.steps;
     s0 = s0 < s1 ? s0 : s1;
-    out += (int64_t)e * p.next_c * ES;
+    out += (int64_t)e * p.m * p.n * ES;
   }
   const uint32_t band = kBand * (uint32_t)p.ntiles, in_band = bid % band;
   const int b0 = (int)(bid / band) * kBand;
@@ -270,8 +268,8 @@ __device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
     if (g.group == p.groups) {  // rows past the last group: zeros
       s1 = 0;
     } else {
-      bskip = (int64_t)g.group * p.b.next;
-      bskip_s = (int64_t)g.group * p.b.next_s;
+      bskip = (int64_t)g.group * p.n * p.b.ld;
+      bskip_s = (int64_t)g.group * p.n * p.b.lds;
     }
   } else {
     m0 = (int64_t)mt * BM;
@@ -408,7 +406,8 @@ struct Feed {
   }
   // CHUNK = 0: thread t prepares row t's.  Rows' lie a row apart in memory, a cache line each, so
   // four blocks' are loaded at once: called for every step, this loads at the first of four
-  // blocks.
+  // blocks.  (Laid out [block][row] by a launch before this one, they cost less here: 539 us against
+  // 555 at 8192 x 8192 x 8192, but with that launch 80 against 73 at 4096 x 4096 x 4096.)
   __device__ __forceinline__ void load_scales(int s) {
     if constexpr (CHUNK > 0) return;
     const int at = s >> shift;
@@ -854,16 +853,11 @@ using namespace tfp8;
 bool product_block_ok(int32_t block) { return block == 128 || block == 256 || block == 512; }
 
 // Launches `kernel` with one workgroup for each of mt x nt tiles (times `times`).
-tfp8_status launch_tiles(void (*kernel)(ProductArgs), ProductArgs p, int bm, int bn, int64_t times,
-                         int threads, hipStream_t st) {
-  // tiles that groups of any sizes can come to, with the rows past the last as one more group
-  const int64_t mt = p.offsets && p.next_c == 0
-                         ? (p.m + (int64_t)(p.groups + 1) * (bm - 1)) / bm
-                         : (p.m + bm - 1) / bm;
-  const int64_t nt = (p.n + bn - 1) / bn;
+tfp8_status launch_tiles(void (*kernel)(ProductArgs), ProductArgs p, int64_t mt, int64_t nt,
+                         int64_t times, int threads, hipStream_t st) {
   if (mt * nt > (((int64_t)1 << 32) - 1) / threads / times) return TFP8_E_SIZE;
-  p.mtiles = (int)mt;
-  p.ntiles = (int)nt;
+  p.mtiles = (int32_t)mt;
+  p.ntiles = (int32_t)nt;
   return launch(kernel, (unsigned)(mt * nt * times), threads, st, p);
 }
 
@@ -889,20 +883,27 @@ int64_t estimate(const Pace &k, int64_t tiles, int64_t steps, int64_t cus) {
 template <int MODE, bool F32OUT>
 tfp8_status launch_product(const ProductArgs &p, hipStream_t st) {
   const int64_t times = MODE == kGroupedDepth ? p.groups : 1, cus = cu_count();
+  const int64_t m = p.m, n = p.n;
   const auto tiles = [&](int bm, int bn) {
-    int64_t mt = (p.m + bm - 1) / bm;
+    int64_t mt = (m + bm - 1) / bm;
     if (MODE == kGroupedRows) mt += p.groups / 2;  // half a tile a group is left over
-    return mt * ((p.n + bn - 1) / bn) * times;
+    return mt * ((n + bn - 1) / bn) * times;
+  };
+  const auto run = [&](void (*kernel)(ProductArgs), int bm, int bn, int threads) {
+    // the tiles that groups of any sizes can come to, with the rows past the last as one more group
+    const int64_t mt = MODE == kGroupedRows ? (m + (int64_t)(p.groups + 1) * (bm - 1)) / bm
+                                            : (m + bm - 1) / bm;
+    return launch_tiles(kernel, p, mt, (n + bn - 1) / bn, times, threads, st);
   };
   if constexpr (MODE != kGroupedDepth) {
     // Few rows that share a B (an even share of them a group): what counts is how many of B's bytes
     // are in flight.  One row of 4096 x 4096: 6.4 us with 16 x 16 tiles, four workgroups a
     // compute unit, 10.6 with 32 x 64; 24 rows of 10240 x 5120: 16.6 us against 15.2.
-    const int64_t together = MODE == kGroupedRows ? (p.m + p.groups - 1) / p.groups : p.m;
+    const int64_t together = MODE == kGroupedRows ? (m + p.groups - 1) / p.groups : m;
     if (together <= 16 || (together <= 64 && tiles(32, 64) < cus / 4))
-      return launch_tiles(k_matmul_split<1, 1, 1, MODE, F32OUT>, p, 16, 16, times, 512, st);
+      return run(k_matmul_split<1, 1, 1, MODE, F32OUT>, 16, 16, 512);
     if (together <= 64)
-      return launch_tiles(k_matmul_split<2, 4, 1, MODE, F32OUT>, p, 32, 64, times, 512, st);
+      return run(k_matmul_split<2, 4, 1, MODE, F32OUT>, 32, 64, 512);
   }
   // Otherwise the kernel whose rounds are done first: large tiles use the matrix cores best, small
   // ones leave less over at the edges and in the last round, and two teams halve the steps of a
@@ -920,7 +921,7 @@ tfp8_status launch_product(const ProductArgs &p, hipStream_t st) {
        {64, 64, 4, 5300, 570, 8500, 1440},
        {64, 64, 2, 5300, 433, 9000, 813}}};
   const int64_t steps =
-      MODE == kGroupedDepth ? (p.rows / p.groups + kStep - 1) / kStep : p.steps;
+      MODE == kGroupedDepth ? ((int64_t)p.rows / p.groups + kStep - 1) / kStep : p.steps;
   int best = 0;
   int64_t least = 0;
   for (int i = 0; i < kKinds; ++i) {
@@ -933,18 +934,15 @@ tfp8_status launch_product(const ProductArgs &p, hipStream_t st) {
     }
   }
   const Pace &k = kPace[F32OUT][best];
-  const auto run = [&](void (*kernel)(ProductArgs), int threads) {
-    return launch_tiles(kernel, p, k.bm, k.bn, times, threads, st);
-  };
   if (best == 0)
     return run(k_matmul_tile<256, F32OUT ? 128 : 256, F32OUT ? 4 : 2, F32OUT ? 2 : 4, 2, 1, 0, MODE,
                              F32OUT>,
-               512);
+               k.bm, k.bn, 512);
   if constexpr (!F32OUT)
-    if (best == 1) return run(k_matmul_tile<128, 128, 2, 4, 2, 1, 0, MODE, F32OUT>, 512);
-  if (best == 2) return run(k_matmul_tile<128, 128, 2, 2, 2, 2, 16, MODE, F32OUT>, 512);
-  if (best == 3) return run(k_matmul_tile<64, 64, 2, 2, 2, 1, 16, MODE, F32OUT>, 256);
-  return run(k_matmul_tile<64, 64, 2, 2, 2, 2, 16, MODE, F32OUT>, 512);
+    if (best == 1) return run(k_matmul_tile<128, 128, 2, 4, 2, 1, 0, MODE, F32OUT>, 128, 128, 512);
+  if (best == 2) return run(k_matmul_tile<128, 128, 2, 2, 2, 2, 16, MODE, F32OUT>, 128, 128, 512);
+  if (best == 3) return run(k_matmul_tile<64, 64, 2, 2, 2, 1, 16, MODE, F32OUT>, 64, 64, 256);
+  return run(k_matmul_tile<64, 64, 2, 2, 2, 2, 16, MODE, F32OUT>, 64, 64, 512);
 }
 
 template <int MODE>
@@ -1014,11 +1012,11 @@ tfp8_status tfp8_matmul(const uint8_t *a_codes, int64_t a_ld, const float *a_alp
   in.add_operand(b_codes, b_alpha, b_scale, n, k, block, b_ld, b_lds);
   if (in.meets(range_of(out, ((m - 1) * ldc + n) * (f32 ? 4 : 2)))) return TFP8_E_ARG;
   ProductArgs p{};
-  p.a = Operand{a_codes, a_alpha, a_scale, a_ld, a_lds, 0, 0};
-  p.b = Operand{b_codes, b_alpha, b_scale, b_ld, b_lds, 0, 0};
-  p.m = m;
-  p.n = n;
-  p.steps = k / kStep;
+  p.a = Operand{a_codes, a_alpha, a_scale, (int32_t)a_ld, (int32_t)a_lds};
+  p.b = Operand{b_codes, b_alpha, b_scale, (int32_t)b_ld, (int32_t)b_lds};
+  p.m = (int32_t)m;
+  p.n = (int32_t)n;
+  p.steps = (int32_t)(k / kStep);
   p.shift = log2_of(block);
   p.out = out;
   p.ldc = ldc;
@@ -1055,11 +1053,11 @@ tfp8_status tfp8_matmul_grouped(const uint8_t *a_codes, int64_t a_ld, const floa
   const Range o = range_of(out, ((m - 1) * ldc + n) * (f32 ? 4 : 2));
   if (in.meets(o) || overlap(o, range_of(offsets, ((int64_t)groups + 1) * 8))) return TFP8_E_ARG;
   ProductArgs p{};
-  p.a = Operand{a_codes, a_alpha, a_scale, a_ld, a_lds, 0, 0};
-  p.b = Operand{b_codes, b_alpha, b_scale, b_ld, b_lds, n * b_ld, n * b_lds};
-  p.m = m;
-  p.n = n;
-  p.steps = k / kStep;
+  p.a = Operand{a_codes, a_alpha, a_scale, (int32_t)a_ld, (int32_t)a_lds};
+  p.b = Operand{b_codes, b_alpha, b_scale, (int32_t)b_ld, (int32_t)b_lds};
+  p.m = (int32_t)m;
+  p.n = (int32_t)n;
+  p.steps = (int32_t)(k / kStep);
   p.shift = log2_of(block);
   p.offsets = offsets;
   p.groups = groups;
@@ -1098,18 +1096,17 @@ tfp8_status tfp8_matmul_grouped_t(const uint8_t *a_codes, int64_t a_ld, const fl
   const Range o = range_of(out, groups * m * n * (f32 ? 4 : 2));
   if (in.meets(o) || overlap(o, range_of(offsets, ((int64_t)groups + 1) * 8))) return TFP8_E_ARG;
   ProductArgs p{};
-  p.a = Operand{a_codes, a_alpha, a_scale, a_ld, a_lds, 0, 0};
-  p.b = Operand{b_codes, b_alpha, b_scale, b_ld, b_lds, 0, 0};
-  p.m = m;
-  p.n = n;
-  p.steps = k / kStep;
+  p.a = Operand{a_codes, a_alpha, a_scale, (int32_t)a_ld, (int32_t)a_lds};
+  p.b = Operand{b_codes, b_alpha, b_scale, (int32_t)b_ld, (int32_t)b_lds};
+  p.m = (int32_t)m;
+  p.n = (int32_t)n;
+  p.steps = (int32_t)(k / kStep);
   p.shift = log2_of(block);
   p.offsets = offsets;
   p.groups = groups;
-  p.rows = rows;
+  p.rows = (int32_t)rows;
   p.out = out;
   p.ldc = n;
-  p.next_c = m * n;
   return launch_product<kGroupedDepth>(p, f32, (hipStream_t)stream);
 }
 
