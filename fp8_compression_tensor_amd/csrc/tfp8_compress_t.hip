@@ -46,7 +46,7 @@ struct TransposeArgs {
   int groups;
   int64_t blocks;  // blocks of an output row
   uint32_t tiles;  // column tiles
-  float TBB, sqrtTB, sqrtTBB, invC;
+  float sqrtTB, sqrtTBB, invC;
   uint8_t *codes;
   float *alpha, *scale;
 };
@@ -268,7 +268,6 @@ tfp8_status tfp8_compress_t(const void *x, tfp8_dtype x_dtype, int64_t rows, int
   p.groups = groups;
   p.blocks = kp / block;
   const double tbb = (double)target * block * (rot ? block : 1);
-  p.TBB = (float)tbb;
   p.sqrtTBB = (float)sqrt(tbb);
   p.sqrtTB = (float)sqrt((double)target * block);
   p.invC = (float)(1.0 / (rot ? 448.0 * sqrt((double)block) : 448.0));

@@ -93,6 +93,11 @@ __device__ __forceinline__ Fragment<WIDE> make_fragment(u32x4 lo, u32x4 hi) {
   return f;
 }
 
+__device__ __forceinline__ f32x4 mfma_codes(const Fragment<false> &x, const Fragment<false> &y) {
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.v, y.v, zero, 0, 0, 0, 0, 0, 0);
+}
+
 // part[j] = x[j] y for all j: the wide form goes over the quarters outermost, so that neighbouring
 // instructions do not wait for one another.
 template <int N>
@@ -111,14 +116,7 @@ template <int N>
 __device__ __forceinline__ void mfma_row(f32x4 (&part)[N], const Fragment<false> (&x)[N],
                                          const Fragment<false> &y) {
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    part[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x[j].v, y.v, zero, 0, 0, 0, 0, 0, 0);
-  }
-}
-__device__ __forceinline__ f32x4 mfma_codes(const Fragment<false> &x, const Fragment<false> &y) {
-  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.v, y.v, zero, 0, 0, 0, 0, 0, 0);
+  for (int j = 0; j < N; ++j) part[j] = mfma_codes(x[j], y);
 }
 
 // A raw buffer descriptor: reads at or past `bytes` give zeros.
@@ -144,11 +142,7 @@ __device__ __forceinline__ void load_to_lds(i32x4 buffer, int voff, int soff, co
       : "memory");
 }
 // Every load of this wavefront, to registers or to LDS, has arrived.
-// All but the last N.
-template <int N = 0>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 // Every LDS access of this wavefront is done,
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 // and those of the whole workgroup.
@@ -288,15 +282,16 @@ __device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
   return true;
 }
 
-// LDS of a tile: NS stages of a step's codes, A's rows then B's, and scales r: those of a step for
-// each stage, or (CHUNK > 0) those of CHUNK blocks.  KS > 1: the workgroup's wavefronts form KS teams
-// with stages of their own, and team g takes steps g, g + KS, ...
-template <int BM_, int BN_, int NS_, int KS_, int CHUNK_>
+// LDS of a tile: two stages of a step's codes, A's rows then B's (three and four measured no
+// faster, and halve what fits), and scales r: those of a step for each stage, or (CHUNK > 0) those of
+// CHUNK blocks.  KS > 1: the workgroup's wavefronts form KS teams with stages of their own, and team
+// g takes steps g, g + KS, ...
+template <int BM_, int BN_, int KS_, int CHUNK_>
 struct Stages {
-  static constexpr int BM = BM_, BN = BN_, NS = NS_, KS = KS_, CHUNK = CHUNK_;
+  static constexpr int BM = BM_, BN = BN_, KS = KS_, CHUNK = CHUNK_;
   static_assert(KS == 1 || CHUNK > 0, "teams share the scales of a chunk");
-  alignas(1024) uint8_t codes[KS][NS][(BM + BN) * kStep];
-  float r[CHUNK ? CHUNK : NS][BM + BN];
+  alignas(1024) uint8_t codes[KS][2][(BM + BN) * kStep];
+  float r[CHUNK ? CHUNK : 2][BM + BN];
 };
 
 // Filling the stages of one team of NW wavefronts.
@@ -454,16 +449,14 @@ __device__ __forceinline__ Fragment<WIDE> read_fragment(const uint8_t *codes, in
 // The loop over steps, for wavefronts of TM x TN tiles.  The scaled addition of a tile's partial
 // products follows TN matrix instructions behind the one that makes them, so that neither waits for
 // the other.  One barrier a step, before the last row of tiles: by then the step's fragments are in
-// registers, so the loads of the step NS ahead may overwrite them, and the next step's first
+// registers, so the loads of the step two ahead may overwrite them, and the next step's first
 // fragments are read under the last row's products.
 template <int TM, int TN, bool WIDE, class STAGES, class FEED>
 __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const ProductArgs &p,
                                           const Job &job, int mrow, int nrow,
                                           f32x4 (&acc)[TM][TN]) {
-  constexpr int NS = STAGES::NS, KS = STAGES::KS, BM = STAGES::BM, CHUNK = STAGES::CHUNK;
-  constexpr bool STEADY = NS > 2 || KS > 1;
+  constexpr int KS = STAGES::KS, BM = STAGES::BM, CHUNK = STAGES::CHUNK;
   constexpr int NP = TM >= 8 ? 3 : TM >= 3 ? 2 : 1;  // a step's loads go out in this many shares
-  constexpr int LOADS = FEED::LA + FEED::LB;
   const int s0 = job.s0, s1 = job.s1;
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
   const int fa0 = fragment_offset(mrow, q, l16), fb0 = fragment_offset(BM + nrow, q, l16);
@@ -471,24 +464,21 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
   const auto &codes = lds.codes[team];
   int s = s0 + team;
   int chunk0 = s0 >> p.shift;  // first block of the scales in LDS (CHUNK)
-  // With more than two stages, or teams, every step issues its loads, past the end those of the last
-  // step again, so that the number in flight is always the same, and a team that is a step short
-  // works on codes (with its scales taken as zero).
+  // With teams every step issues its loads, past the end those of the last step again, so that a
+  // team that is a step short works on codes (with its scales taken as zero).
   const auto load = [&](int x, int slot, int part, int parts) {
-    if (STEADY)
+    if (KS > 1)
       feed.load_step(x < s1 ? x : s1 - 1, slot, part, parts);
     else if (x < s1)
       feed.load_step(x, slot, part, parts);
   };
   feed.load_scales(s);
-#pragma unroll
-  for (int k = 0; k < NS - 1; ++k) load(s + k * KS, k, 0, 1);
-  if (NS == 2) wait_loads();
+  load(s, 0, 0, 1);
+  wait_loads();
   feed.put_scales(s, 0);
   if constexpr (CHUNK > 0) feed.fill_scales(chunk0, p, job);
-  wait_loads<(NS - 2) * LOADS>();
   lds_barrier();
-  load(s + (NS - 1) * KS, NS - 1, 0, NP);
+  load(s + KS, 1, 0, NP);
   if (NP == 1 && s + 1 < s1) feed.load_scales(s + 1);
   // where the scales of step x, in slot y, are
   const auto scales = [&](int x, int y) {
@@ -512,18 +502,16 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
     // every partial product until then
     asm volatile("" : "+v"(to[j]));
   };
-  const auto next = [](int slot) { return NS == 2 ? slot ^ 1 : slot + 1 < NS ? slot + 1 : 0; };
-  for (int slot = 0; s - team < s1; s += KS, slot = next(slot)) {
-    const int ahead = next(slot);
-    const int back = NS == 2 ? ahead : slot ? slot - 1 : NS - 1;  // of the step NS - 1 ahead
+  for (int slot = 0; s - team < s1; s += KS, slot ^= 1) {
+    const int ahead = slot ^ 1;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const bool last = i == TM - 1;
       if (last) {
-        wait_loads<(NS - 2) * LOADS>();
+        wait_loads();
         if (s + 1 < s1) feed.put_scales(s + 1, ahead);
         lds_barrier();
-        load(s + NS * KS, slot, 0, NP);
+        load(s + 2 * KS, slot, 0, NP);
         if (NP == 1 && s + 2 < s1) feed.load_scales(s + 2);
         if constexpr (CHUNK > 0) {
           const int n0 = s - team + KS, n1 = n0 + KS - 1;  // the teams' next steps
@@ -534,7 +522,7 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
           }
         }
       } else if (i + 1 < NP) {
-        load(s + (NS - 1) * KS, back, i + 1, NP);
+        load(s + KS, ahead, i + 1, NP);
         if (i + 2 == NP && s + 1 < s1) feed.load_scales(s + 1);
       }
       const int ns = last ? ahead : slot;
@@ -573,15 +561,15 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
   }
 #pragma unroll
   for (int j = 0; j < TN; ++j) add_part(acc[TM - 1], j);
-  if (STEADY) wait_loads();  // no load may arrive after the workgroup has given its LDS back
+  if (KS > 1) wait_loads();  // no load may arrive after the workgroup has given its LDS back
 }
 
 // The kernel only calls this function: a kernel's own body is also read by the host's pass, which
 // does not know these builtins.
-template <int BM, int BN, int WM, int WN, int NS, int KS, int CHUNK, int MODE, bool F32OUT>
+template <int BM, int BN, int WM, int WN, int KS, int CHUNK, int MODE, bool F32OUT>
 __device__ __forceinline__ void matmul_tile(const ProductArgs &p) {
   constexpr int TM = BM / 16 / WM, TN = BN / 16 / WN, KEEP = TM / KS;
-  using STAGES = Stages<BM, BN, NS, KS, CHUNK>;
+  using STAGES = Stages<BM, BN, KS, CHUNK>;
   __shared__ STAGES lds;
   Job t;
   if (!find_job<BM, BN, MODE, F32OUT ? 4 : 2>(p, t)) return;
@@ -649,21 +637,20 @@ __device__ __forceinline__ void matmul_tile(const ProductArgs &p) {
   }
 }
 
-template <int BM, int BN, int WM, int WN, int NS, int KS, int CHUNK, int MODE, bool F32OUT>
+template <int BM, int BN, int WM, int WN, int KS, int CHUNK, int MODE, bool F32OUT>
 __global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_matmul_tile(ProductArgs p) {
-  matmul_tile<BM, BN, WM, WN, NS, KS, CHUNK, MODE, F32OUT>(p);
+  matmul_tile<BM, BN, WM, WN, KS, CHUNK, MODE, F32OUT>(p);
 }
 
 // --------------------------------------------------------------------------------------------
 // Few rows (decoding): B's bytes bound the product.  A workgroup takes one tile of 16 MT rows of A
 // (its group's) by 16 TN of B, and its eight wavefronts divide the depth: each computes the whole tile
 // over its share of the steps, and the eight are added up through LDS in a fixed order at the end.
-// Each wavefront has ST stages of LDS to itself, so there is no barrier in the loop: it waits for
-// its own loads alone, reads a step's fragments into registers, and sends the stage's next loads
-// out before it multiplies.  (Fragments loaded straight from memory, 16 rows of 64 bytes an
+// Each wavefront has a stage of LDS to itself, so there is no barrier in the loop: it waits for
+// its own loads alone, reads a step's codes into registers, and sends the next step's loads out before
+// it multiplies.  (Fragments loaded straight from memory, 16 rows of 64 bytes an
 // instruction in the order of the lanes, come at 9.6 TB/s over the chip, from the L1 cache too; whole
-// lines through LDS come at 28.)  With one stage, the next step's fragments are read under this
-// one's products.  Scales are prepared in LDS, kSplitBlocks blocks at a time.
+// lines through LDS come at 28.)  Scales are prepared in LDS, kSplitBlocks blocks at a time.
 constexpr int kSplitWaves = 8, kSplitBlocks = 64;
 
 // 32 codes of a lane, as stored.
@@ -674,14 +661,14 @@ __device__ __forceinline__ Codes read_codes(const uint8_t *codes, int at) {
   return Codes{*(const u32x4 *)(codes + at), *(const u32x4 *)(codes + (at ^ 64))};
 }
 
-template <int MT, int TN, int ST, int MODE, bool F32OUT>
+template <int MT, int TN, int MODE, bool F32OUT>
 __device__ __forceinline__ void matmul_split(const ProductArgs &p) {
   constexpr int BM = 16 * MT, BN = 16 * TN, ROWS = BM + BN, NT = 64 * kSplitWaves;
   constexpr int QUADS = kSplitBlocks / 4, EACH = (ROWS * QUADS + NT - 1) / NT;
   constexpr int LOADS = ROWS / 8;  // a step's
   __shared__ struct {
     union {
-      alignas(1024) uint8_t codes[kSplitWaves][ST][ROWS * kStep];
+      alignas(1024) uint8_t codes[kSplitWaves][ROWS * kStep];
       f32x4 sum[kSplitWaves][MT * TN][64];
     };
     float r[kSplitBlocks][ROWS];
@@ -703,19 +690,19 @@ __device__ __forceinline__ void matmul_split(const ProductArgs &p) {
     const int left = ((isa ? t.mv : t.nv) - 1 - row) * ld + (int)p.steps * kStep;
     from[i] = buffer_of((isa ? t.ac : t.bc) + row * ld, left > 0 ? left : 0);
   }
-  const auto load = [&](int s, int slot) {  // past the end: the last step again, which is left out
+  const auto load = [&](int s) {  // past the end: the last step again, which is left out
     const int k0 = (s < t.s1 ? s : t.s1 - 1) * kStep;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i)
-      load_to_lds(from[i], i < BM / 8 ? va : vb, k0, &lds.codes[w][slot][i * 1024]);
+      load_to_lds(from[i], i < BM / 8 ? va : vb, k0, &lds.codes[w][i * 1024]);
   };
   const int fa0 = fragment_offset(0, q, l16), fb0 = fragment_offset(BM, q, l16);
   Codes ca[MT], cb[TN];
-  const auto read = [&](int slot) {
+  const auto read = [&] {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) cb[j] = read_codes(lds.codes[w][slot], fb0 + j * 16 * kStep);
+    for (int j = 0; j < TN; ++j) cb[j] = read_codes(lds.codes[w], fb0 + j * 16 * kStep);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) ca[i] = read_codes(lds.codes[w][slot], fa0 + i * 16 * kStep);
+    for (int i = 0; i < MT; ++i) ca[i] = read_codes(lds.codes[w], fa0 + i * 16 * kStep);
   };
   f32x4 acc[MT][TN];
 #pragma unroll
@@ -730,8 +717,7 @@ __device__ __forceinline__ void matmul_split(const ProductArgs &p) {
     const int share = (c1 - c0 + kSplitWaves - 1) / kSplitWaves;
     int s = c0 + w * share;
     const int e = s + share < c1 ? s + share : c1;
-#pragma unroll
-    for (int k = 0; k < ST; ++k) load(s + k, k);
+    load(s);
     const int b0 = c0 >> p.shift;
     if (c0 != t.s0) __syncthreads();  // the scales before are no longer read
     f32x4 x[EACH], y[EACH];
@@ -768,8 +754,7 @@ __device__ __forceinline__ void matmul_split(const ProductArgs &p) {
         for (int u = 0; u < 4; ++u) lds.r[k + u][row] = x[i][u] * __builtin_amdgcn_rcpf(y[i][u]);
     }
     __syncthreads();
-    const auto multiply = [&](const Codes (&xa)[MT], const Codes (&xb)[TN], int step, int i0,
-                              int i1) {
+    const auto multiply = [&](const Codes (&xa)[MT], const Codes (&xb)[TN], int step) {
       const float *r = lds.r[(step >> p.shift) - b0];
       Fragment<F32OUT> fb[TN];
       f32x4 rb[TN];
@@ -779,7 +764,7 @@ __device__ __forceinline__ void matmul_split(const ProductArgs &p) {
         rb[j] = *(const f32x4 *)&r[BM + j * 16 + 4 * q];
       }
 #pragma unroll
-      for (int i = i0; i < i1; ++i) {
+      for (int i = 0; i < MT; ++i) {
         const Fragment<F32OUT> fa = make_fragment<F32OUT>(xa[i].lo, xa[i].hi);
         const float ra = r[i * 16 + l16];
         f32x4 part[TN];
@@ -791,34 +776,21 @@ __device__ __forceinline__ void matmul_split(const ProductArgs &p) {
             acc[i][j][k] = fmaf(part[j][k], ra * rb[j][k], acc[i][j][k]);
       }
     };
-    if constexpr (ST == 1) {
-      wait_loads();
-      read(0);
-      for (; s < e; ++s) {
-        Codes xa[MT], xb[TN];
+    wait_loads();
+    read();
+    for (; s < e; ++s) {
+      Codes xa[MT], xb[TN];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) xb[j] = cb[j];
+      for (int j = 0; j < TN; ++j) xb[j] = cb[j];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) xa[i] = ca[i];
-        wait_lds();
-        load(s + 1, 0);
-        multiply(xa, xb, s, 0, MT);
-        wait_loads();
-        read(0);
-      }
+      for (int i = 0; i < MT; ++i) xa[i] = ca[i];
       wait_lds();
-    } else {
-      int slot = 0;
-      for (; s < e; ++s) {
-        wait_loads<(ST - 1) * LOADS>();
-        read(slot);
-        wait_lds();
-        load(s + ST, slot);
-        multiply(ca, cb, s, 0, MT);
-        slot = slot + 1 < ST ? slot + 1 : 0;
-      }
+      load(s + 1);
+      multiply(xa, xb, s);
       wait_loads();
+      read();
     }
+    wait_lds();
   }
   __syncthreads();
 #pragma unroll
@@ -839,9 +811,9 @@ __device__ __forceinline__ void matmul_split(const ProductArgs &p) {
   }
 }
 
-template <int MT, int TN, int ST, int MODE, bool F32OUT>
+template <int MT, int TN, int MODE, bool F32OUT>
 __global__ __launch_bounds__(64 * kSplitWaves, 2) void k_matmul_split(ProductArgs p) {
-  matmul_split<MT, TN, ST, MODE, F32OUT>(p);
+  matmul_split<MT, TN, MODE, F32OUT>(p);
 }
 
 }  // namespace tfp8
@@ -901,9 +873,9 @@ tfp8_status launch_product(const ProductArgs &p, hipStream_t st) {
     // compute unit, 10.6 with 32 x 64; 24 rows of 10240 x 5120: 16.6 us against 15.2.
     const int64_t together = MODE == kGroupedRows ? (m + p.groups - 1) / p.groups : m;
     if (together <= 16 || (together <= 64 && tiles(32, 64) < cus / 4))
-      return run(k_matmul_split<1, 1, 1, MODE, F32OUT>, 16, 16, 512);
+      return run(k_matmul_split<1, 1, MODE, F32OUT>, 16, 16, 512);
     if (together <= 64)
-      return run(k_matmul_split<2, 4, 1, MODE, F32OUT>, 32, 64, 512);
+      return run(k_matmul_split<2, 4, MODE, F32OUT>, 32, 64, 512);
   }
   // Otherwise the kernel whose rounds are done first: large tiles use the matrix cores best, small
   // ones leave less over at the edges and in the last round, and two teams halve the steps of a
@@ -935,14 +907,14 @@ tfp8_status launch_product(const ProductArgs &p, hipStream_t st) {
   }
   const Pace &k = kPace[F32OUT][best];
   if (best == 0)
-    return run(k_matmul_tile<256, F32OUT ? 128 : 256, F32OUT ? 4 : 2, F32OUT ? 2 : 4, 2, 1, 0, MODE,
+    return run(k_matmul_tile<256, F32OUT ? 128 : 256, F32OUT ? 4 : 2, F32OUT ? 2 : 4, 1, 0, MODE,
                              F32OUT>,
                k.bm, k.bn, 512);
   if constexpr (!F32OUT)
-    if (best == 1) return run(k_matmul_tile<128, 128, 2, 4, 2, 1, 0, MODE, F32OUT>, 128, 128, 512);
-  if (best == 2) return run(k_matmul_tile<128, 128, 2, 2, 2, 2, 16, MODE, F32OUT>, 128, 128, 512);
-  if (best == 3) return run(k_matmul_tile<64, 64, 2, 2, 2, 1, 16, MODE, F32OUT>, 64, 64, 256);
-  return run(k_matmul_tile<64, 64, 2, 2, 2, 2, 16, MODE, F32OUT>, 64, 64, 512);
+    if (best == 1) return run(k_matmul_tile<128, 128, 2, 4, 1, 0, MODE, F32OUT>, 128, 128, 512);
+  if (best == 2) return run(k_matmul_tile<128, 128, 2, 2, 2, 16, MODE, F32OUT>, 128, 128, 512);
+  if (best == 3) return run(k_matmul_tile<64, 64, 2, 2, 1, 16, MODE, F32OUT>, 64, 64, 256);
+  return run(k_matmul_tile<64, 64, 2, 2, 2, 16, MODE, F32OUT>, 64, 64, 512);
 }
 
 template <int MODE>
