@@ -36,31 +36,53 @@ struct GroupTile {
   int group;
 };
 
-// The idx-th tile of at most `size` rows, counting the tiles of group 0, 1, ... up to group
-// `last` (last = groups counts the rows past the last group as one more group).
+// 64 groups, one a lane: their rows, their tiles of at most `size` rows, and the sum of these up to
+// the lane's own (of groups that do not overlap; the sum of others may wrap).
+struct GroupScan {
+  int lo, hi, tiles, incl;
+};
+__device__ __forceinline__ GroupScan scan_groups(const int64_t *offsets, int groups, int64_t rows,
+                                                 int size, int g0, int last) {
+  const int lane = threadIdx.x & 63, e = g0 + lane;
+  GroupScan s{0, 0, 0, 0};
+  if (e <= last) group_rows(offsets, groups, rows, e, s.lo, s.hi);
+  s.tiles = (int)(((int64_t)(s.hi - s.lo) + size - 1) / size);
+  s.incl = wave_inclusive_sum(s.tiles, lane);
+  return s;
+}
+
+// A tile of at most `size` rows, counting the tiles of group 0, 1, ... up to group `last` (last =
+// groups counts the rows past the last group as one more group): the one that pick(how many there
+// are) names.
+template <class PICK>
 __device__ __forceinline__ GroupTile tile_of_groups(const int64_t *offsets, int groups,
-                                                    int64_t rows, int size, int64_t idx,
-                                                    int last) {
-  const int lane = threadIdx.x & 63;
+                                                    int64_t rows, int size, int last, PICK pick) {
+  GroupScan s = scan_groups(offsets, groups, rows, size, 0, last);
+  int64_t all = __builtin_amdgcn_readfirstlane(__shfl(s.incl, 63));
+  for (int g0 = 64; g0 <= last; g0 += 64)
+    all += __builtin_amdgcn_readfirstlane(
+        __shfl(scan_groups(offsets, groups, rows, size, g0, last).incl, 63));
+  const int64_t idx = pick(all);
   int64_t before = 0;
-  for (int g0 = 0; g0 <= last; g0 += 64) {
-    const int e = g0 + lane;
-    int lo = 0, hi = 0;
-    if (e <= last) group_rows(offsets, groups, rows, e, lo, hi);
-    const int tiles = (int)(((int64_t)(hi - lo) + size - 1) / size);
-    const int incl = wave_inclusive_sum(tiles, lane);  // <= 64 * 2^31 / size
-    const uint64_t past = __ballot(before + incl > idx);
+  for (int g0 = 0;;) {
+    const uint64_t past = __ballot(before + s.incl > idx);
     if (past) {
       const int f = __builtin_ctzll(past);
-      const int t = (int)(idx - before) - (__shfl(incl, f) - __shfl(tiles, f));
-      const int l = __shfl(lo, f), h = __shfl(hi, f);
+      const int tiles = __builtin_amdgcn_readfirstlane(__shfl(s.tiles, f));
+      const int t =
+          __builtin_amdgcn_readfirstlane((int)(idx - before) - (__shfl(s.incl, f) - tiles));
+      const int l = __shfl(s.lo, f), h = __shfl(s.hi, f);
+      if ((uint32_t)t >= (uint32_t)tiles) break;  // wrapped sums
       GroupTile r;
       r.row0 = __builtin_amdgcn_readfirstlane(l + t * size);
       r.rows = __builtin_amdgcn_readfirstlane(h - r.row0 < size ? h - r.row0 : size);
       r.group = __builtin_amdgcn_readfirstlane(g0 + f);
       return r;
     }
-    before += __shfl(incl, 63);
+    before += __builtin_amdgcn_readfirstlane(__shfl(s.incl, 63));
+    g0 += 64;
+    if (g0 > last) break;
+    s = scan_groups(offsets, groups, rows, size, g0, last);
   }
   return GroupTile{0, 0, 0};
 }

@@ -229,33 +229,38 @@ struct Job {
 // ragged depths would be uneven (561 us against 454), and stay in plain order.
 constexpr int kBand = 4;
 
+// This workgroup's place among `all` tiles (at most one a workgroup); all: it has none.
+__device__ __forceinline__ uint32_t place_of_workgroup(uint32_t all) {
+  const uint32_t per = all >> 3, over = all & 7, x = blockIdx.x & 7, i = blockIdx.x >> 3;
+  return i < per + (x < over) ? x * per + (x < over ? x : over) + i : all;
+}
+
+// Row and column of tiles of place `at` in mtiles rows of ntiles.
+__device__ __forceinline__ void tile_at(uint32_t at, int mtiles, int ntiles, int &mt, int &nt) {
+  const uint32_t band = kBand * (uint32_t)ntiles, in_band = at % band;
+  const int b0 = (int)(at / band) * kBand;
+  const uint32_t high = mtiles - b0 < kBand ? mtiles - b0 : kBand;
+  mt = b0 + (int)(in_band % high);
+  nt = (int)(in_band / high);
+}
+
 template <int BM, int BN, int MODE, int ES>
 __device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
-  uint32_t bid = blockIdx.x;
-  if constexpr (MODE != kGroupedDepth) {
-    const uint32_t per = gridDim.x >> 3, over = gridDim.x & 7, x = blockIdx.x & 7;
-    bid = x * per + (x < over ? x : over) + (blockIdx.x >> 3);
-  }
   char *out = (char *)p.out;
-  int64_t s0 = 0, s1 = p.steps;
-  if constexpr (MODE == kGroupedDepth) {
-    const uint32_t per = (uint32_t)p.mtiles * p.ntiles, e = bid / per;
-    bid -= e * per;
-    const GroupSpan g = span_of_group(p.offsets, p.groups, p.rows, kStep << p.shift, (int)e);
-    s0 = g.unit0 << p.shift;
-    s1 = (g.unit0 + g.units) << p.shift;
-    s1 = s1 < p.steps ? s1 : p.steps;
-    s0 = s0 < s1 ? s0 : s1;
-    out += (int64_t)e * p.m * p.n * ES;
-  }
-  const uint32_t band = kBand * (uint32_t)p.ntiles, in_band = bid % band;
-  const int b0 = (int)(bid / band) * kBand;
-  const uint32_t high = p.mtiles - b0 < kBand ? p.mtiles - b0 : kBand;
-  const int mt = b0 + (int)(in_band % high), nt = (int)(in_band / high);
-  const int64_t n0 = (int64_t)nt * BN;
-  int64_t m0, bskip = 0, bskip_s = 0;
+  int64_t s0 = 0, s1 = p.steps, m0, bskip = 0, bskip_s = 0;
+  int mt = 0, nt = 0;
   if constexpr (MODE == kGroupedRows) {
-    const GroupTile g = tile_of_groups(p.offsets, p.groups, p.m, BM, mt, p.groups);
+    // the launch is for the most tiles that groups of any sizes come to; the parts are of those
+    // that there are (3200 rows in 16 groups by 2560 x 2048: 43 us, against 83 in parts of the launch,
+    // which left the last XCD without work)
+    const GroupTile g =
+        tile_of_groups(p.offsets, p.groups, p.m, BM, p.groups, [&](int64_t there) -> int64_t {
+          const int mtiles = there < p.mtiles ? (int)there : p.mtiles;  // more: overlapping groups
+          const uint32_t all = (uint32_t)mtiles * p.ntiles, at = place_of_workgroup(all);
+          if (at >= all) return there;
+          tile_at(at, mtiles, p.ntiles, mt, nt);
+          return mt;
+        });
     if (g.rows <= 0) return false;
     m0 = g.row0;
     t.mv = g.rows;
@@ -266,9 +271,24 @@ __device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
       bskip_s = (int64_t)g.group * p.n * p.b.lds;
     }
   } else {
+    uint32_t at = blockIdx.x;
+    if constexpr (MODE == kGroupedDepth) {
+      const uint32_t per = (uint32_t)p.mtiles * p.ntiles, e = at / per;
+      at -= e * per;
+      const GroupSpan g = span_of_group(p.offsets, p.groups, p.rows, kStep << p.shift, (int)e);
+      s0 = g.unit0 << p.shift;
+      s1 = (g.unit0 + g.units) << p.shift;
+      s1 = s1 < p.steps ? s1 : p.steps;
+      s0 = s0 < s1 ? s0 : s1;
+      out += (int64_t)e * p.m * p.n * ES;
+    } else {
+      at = place_of_workgroup(gridDim.x);
+    }
+    tile_at(at, p.mtiles, p.ntiles, mt, nt);
     m0 = (int64_t)mt * BM;
     t.mv = (int)(p.m - m0 < BM ? p.m - m0 : BM);
   }
+  const int64_t n0 = (int64_t)nt * BN;
   t.nv = (int)(p.n - n0 < BN ? p.n - n0 : BN);
   t.s0 = (int)s0;
   t.s1 = (int)s1;
@@ -282,7 +302,7 @@ __device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
   return true;
 }
 
-// LDS of a tile: two stages of a step's codes, A's rows then B's (three and four measured no
+// LDS of a tile: two stages of a step's codes, A's rows then B's (four measured no
 // faster, and halve what fits), and scales r: those of a step for each stage, or (CHUNK > 0) those of
 // CHUNK blocks.  KS > 1: the workgroup's wavefronts form KS teams with stages of their own, and team
 // g takes steps g, g + KS, ...
@@ -564,6 +584,23 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
   if (KS > 1) wait_loads();  // no load may arrive after the workgroup has given its LDS back
 }
 
+// One tile of BM x BN by WM x WN wavefronts (of KS teams).
+//
+// What bounds it.  bfloat16, tiles of 256 x 256: a matrix instruction takes 32 cycles of its unit, and
+// with the eight vector instructions of its scaled addition 48 of its SIMD.  8192 x 16384 x 4096 in
+// blocks of 256 takes 560 to 620 us on different cards, 1.77 to 1.96 PFLOP/s (a library product of
+// 8-bit operands with one scale each reaches 3.1): 4540 cycles a step, 2048 of them the matrix
+// units', at a clock that the power limit holds near 1.9 GHz.  Codes that are all zero take 13% less
+// time at the same work, and a loop over tiles that fetches the next one's codes under the stores of
+// this one gained nothing.  16384 rows in 8 groups by 5120 x 4096: 435 to 485 us, the same rate less
+// its last round of tiles, a third full.
+// float32, tiles of 256 x 128: widening the codes takes eight more vector instructions for each 16 x
+// 16 tile and step, and the matrix instructions have half the rate.  8 groups of 16384 rows in all,
+// 4096 x 2560 each: 413 to 465 us, 0.74 to 0.83 PFLOP/s; a tile is 16 steps deep there, 41 us, of which
+// 8.6 are its start, its first loads and its stores.  In tiles of 64 x 64 (1003 x 2571 x 2560: 25 us)
+// widening is what bounds it: 64 of a wavefront's 104 vector instructions a step, for four 16 x 16
+// tiles; larger tiles, which widen less, leave compute units without one.
+//
 // The kernel only calls this function: a kernel's own body is also read by the host's pass, which
 // does not know these builtins.
 template <int BM, int BN, int WM, int WN, int KS, int CHUNK, int MODE, bool F32OUT>
@@ -650,7 +687,12 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_matmul_tile(ProductArg
 // its own loads alone, reads a step's codes into registers, and sends the next step's loads out before
 // it multiplies.  (Fragments loaded straight from memory, 16 rows of 64 bytes an
 // instruction in the order of the lanes, come at 9.6 TB/s over the chip, from the L1 cache too; whole
-// lines through LDS come at 28.)  Scales are prepared in LDS, kSplitBlocks blocks at a time.
+// lines through LDS come at 28.)
+//
+// 24 x 10240 x 5120: 13.9 us, 4.1 TB/s, in 32 x 48 tiles (14.5 in 32 x 64, 19 in 32 x 32, whose 320
+// workgroups are more than one round); 48 rows in 16 groups, 2560 x 4096 each: 36 us, 4.7 TB/s, where a
+// large copy reaches 5.0.  One row of 4096 x 4096, 2.9 TB/s, takes 6.2 us, of which its bytes are 3.6
+// and the start, the first loads' latency and the sum over the wavefronts the rest.  Scales are prepared in LDS, kSplitBlocks blocks at a time.
 constexpr int kSplitWaves = 8, kSplitBlocks = 64;
 
 // 32 codes of a lane, as stored.
@@ -833,13 +875,32 @@ tfp8_status launch_tiles(void (*kernel)(ProductArgs), ProductArgs p, int64_t mt,
   return launch(kernel, (unsigned)(mt * nt * times), threads, st, p);
 }
 
-// How long a kernel takes for tiles of bm x bn, by what a round of its workgroups took in products of
-// 1024 to 4096 rows and columns and 1024 to 4096 codes deep (ns): `first` and `step` a step where
-// every compute unit has one workgroup, and the same where it has all `slots` that fit.
+// How long a kernel takes for tiles of bm x bn (ns): `first` and `step` a step where every compute
+// unit has one workgroup, and the same where it has all `slots` that fit.  From the times of 512 products
+// of each output type, of 1 to 4096 rows and 512 to 16384 columns, 640 to 5120 deep, dense, in 4
+// to 32 groups and by groups along the depth, a fifth of them with operands that no cache holds; fitted
+// so that the choice below costs least: what it picks takes 0.8% longer than the best of these
+// kernels on average for bfloat16 outputs, 1.1% for float32 (a choice by the number of rows alone took
+// 20% longer, up to 4 times as long).
 struct Pace {
   int bm, bn, slots;
   int64_t first, step, first_full, step_full;
 };
+enum : int { kLarge, kMiddle, kSmall, kSmallTeams, kFew, kFew32, kFew48, kKinds };
+constexpr Pace kPace[2][kKinds] = {{{256, 256, 1, 11410, 2320, 11410, 2320},
+                                    {128, 128, 2, 3590, 1310, 5590, 1450},
+                                    {64, 64, 4, 2330, 460, 4230, 1290},
+                                    {64, 64, 2, 3080, 360, 4610, 690},
+                                    {16, 16, 4, 3010, 17, 4290, 251},
+                                    {32, 32, 2, 3670, 95, 5310, 277},
+                                    {32, 48, 1, 3250, 160, 3250, 160}},
+                                   {{256, 128, 1, 9340, 1910, 9340, 1910},
+                                    {},  // 128 x 128: first in 2% of the float32 products only
+                                    {64, 64, 4, 2690, 560, 6420, 1280},
+                                    {64, 64, 2, 3660, 420, 8100, 1080},
+                                    {16, 16, 4, 2680, 30, 4910, 260},
+                                    {32, 32, 2, 3930, 107, 4980, 243},
+                                    {32, 48, 1, 3710, 153, 3710, 153}}};
 
 int64_t estimate(const Pace &k, int64_t tiles, int64_t steps, int64_t cus) {
   const int64_t one = k.first + steps * k.step, full = k.first_full + steps * k.step_full;
@@ -852,69 +913,51 @@ int64_t estimate(const Pace &k, int64_t tiles, int64_t steps, int64_t cus) {
   return t;
 }
 
+// The kernel whose rounds of workgroups are done first: large tiles use the matrix cores best, small
+// ones leave less over at the edges and in the last round, two teams halve the steps of a product
+// with few tiles, and the kernels for few rows divide them by eight.
 template <int MODE, bool F32OUT>
 tfp8_status launch_product(const ProductArgs &p, hipStream_t st) {
   const int64_t times = MODE == kGroupedDepth ? p.groups : 1, cus = cu_count();
   const int64_t m = p.m, n = p.n;
-  const auto tiles = [&](int bm, int bn) {
-    int64_t mt = (m + bm - 1) / bm;
-    if (MODE == kGroupedRows) mt += p.groups / 2;  // half a tile a group is left over
-    return mt * ((n + bn - 1) / bn) * times;
-  };
-  const auto run = [&](void (*kernel)(ProductArgs), int bm, int bn, int threads) {
+  const int64_t steps =
+      MODE == kGroupedDepth ? ((int64_t)p.rows / p.groups + kStep - 1) / kStep : p.steps;
+  int best = -1;
+  int64_t least = 0;
+  for (int i = 0; i < (MODE == kGroupedDepth ? kFew : kKinds); ++i) {
+    const Pace &k = kPace[F32OUT][i];
+    if (k.slots == 0) continue;
+    int64_t mt = (m + k.bm - 1) / k.bm;
+    if (MODE == kGroupedRows) {  // a tile for each group, and half of one more on average
+      const int64_t least_mt = m < p.groups ? m : p.groups;
+      mt = m / k.bm + p.groups / 2;
+      mt = mt < least_mt ? least_mt : mt;
+    }
+    const int64_t ns = estimate(k, mt * ((n + k.bn - 1) / k.bn) * times, steps, cus);
+    if (best < 0 || ns < least) {
+      best = i;
+      least = ns;
+    }
+  }
+  const int bm = kPace[F32OUT][best].bm, bn = kPace[F32OUT][best].bn;
+  const auto run = [&](void (*kernel)(ProductArgs), int threads) {
     // the tiles that groups of any sizes can come to, with the rows past the last as one more group
     const int64_t mt = MODE == kGroupedRows ? (m + (int64_t)(p.groups + 1) * (bm - 1)) / bm
                                             : (m + bm - 1) / bm;
     return launch_tiles(kernel, p, mt, (n + bn - 1) / bn, times, threads, st);
   };
   if constexpr (MODE != kGroupedDepth) {
-    // Few rows that share a B (an even share of them a group): what counts is how many of B's bytes
-    // are in flight.  One row of 4096 x 4096: 6.4 us with 16 x 16 tiles, four workgroups a
-    // compute unit, 10.6 with 32 x 64; 24 rows of 10240 x 5120: 16.6 us against 15.2.
-    const int64_t together = MODE == kGroupedRows ? (m + p.groups - 1) / p.groups : m;
-    if (together <= 16 || (together <= 64 && tiles(32, 64) < cus / 4))
-      return run(k_matmul_split<1, 1, MODE, F32OUT>, 16, 16, 512);
-    if (together <= 64)
-      return run(k_matmul_split<2, 4, MODE, F32OUT>, 32, 64, 512);
+    if (best == kFew) return run(k_matmul_split<1, 1, MODE, F32OUT>, 512);
+    if (best == kFew32) return run(k_matmul_split<2, 2, MODE, F32OUT>, 512);
+    if (best == kFew48) return run(k_matmul_split<2, 3, MODE, F32OUT>, 512);
   }
-  // Otherwise the kernel whose rounds are done first: large tiles use the matrix cores best, small
-  // ones leave less over at the edges and in the last round, and two teams halve the steps of a
-  // product with about as many tiles as compute units.
-  constexpr int kKinds = 5;
-  constexpr Pace kPace[2][kKinds] = {
-      {{256, 256, 1, 9700, 2060, 9700, 2060},
-       {128, 128, 2, 5000, 840, 7500, 1300},
-       {128, 128, 1, 8000, 620, 8000, 620},  // two teams
-       {64, 64, 4, 4200, 460, 6200, 900},
-       {64, 64, 2, 4500, 334, 6250, 448}},   // two teams
-      {{256, 128, 1, 8600, 2000, 8600, 2000},
-       {0, 0, 0, 0, 0, 0, 0},
-       {128, 128, 1, 8800, 1087, 8800, 1087},
-       {64, 64, 4, 5300, 570, 8500, 1440},
-       {64, 64, 2, 5300, 433, 9000, 813}}};
-  const int64_t steps =
-      MODE == kGroupedDepth ? ((int64_t)p.rows / p.groups + kStep - 1) / kStep : p.steps;
-  int best = 0;
-  int64_t least = 0;
-  for (int i = 0; i < kKinds; ++i) {
-    const Pace &k = kPace[F32OUT][i];
-    if (k.slots == 0) continue;  // no sizes at which 128 x 128 without teams would be first
-    const int64_t ns = estimate(k, tiles(k.bm, k.bn), steps, cus);
-    if (i == 0 || ns < least) {
-      best = i;
-      least = ns;
-    }
-  }
-  const Pace &k = kPace[F32OUT][best];
-  if (best == 0)
-    return run(k_matmul_tile<256, F32OUT ? 128 : 256, F32OUT ? 4 : 2, F32OUT ? 2 : 4, 1, 0, MODE,
-                             F32OUT>,
-               k.bm, k.bn, 512);
   if constexpr (!F32OUT)
-    if (best == 1) return run(k_matmul_tile<128, 128, 2, 4, 1, 0, MODE, F32OUT>, 128, 128, 512);
-  if (best == 2) return run(k_matmul_tile<128, 128, 2, 2, 2, 16, MODE, F32OUT>, 128, 128, 512);
-  if (best == 3) return run(k_matmul_tile<64, 64, 2, 2, 1, 16, MODE, F32OUT>, 64, 64, 256);
-  return run(k_matmul_tile<64, 64, 2, 2, 2, 16, MODE, F32OUT>, 64, 64, 512);
+    if (best == kMiddle) return run(k_matmul_tile<128, 128, 2, 4, 1, 0, MODE, F32OUT>, 512);
+  if (best == kSmall) return run(k_matmul_tile<64, 64, 2, 2, 1, 16, MODE, F32OUT>, 256);
+  if (best == kSmallTeams) return run(k_matmul_tile<64, 64, 2, 2, 2, 16, MODE, F32OUT>, 512);
+  return run(k_matmul_tile<256, F32OUT ? 128 : 256, F32OUT ? 4 : 2, F32OUT ? 2 : 4, 1, 0, MODE,
+                           F32OUT>,
+             512);
 }
 
 template <int MODE>
