@@ -477,26 +477,22 @@ def _operand(t, block: int, dims: int, name: str):
 
 
 def _product_out(out, shape, dtype: torch.dtype, a, b):
-    """The output, new or checked, of a product of a and b, whose devices are compared."""
+    """(the output, its row stride) of a product of a and b, whose devices are compared: a new
+    tensor, or `out` checked, whose rows must be contiguous."""
     if a[0].get_device() != b[0].get_device():
         raise ValueError(f"tensors on different devices ({a[0].device} and {b[0].device})")
     device = a[0].device
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device), shape[-1]
     if not (isinstance(out, torch.Tensor) and out.is_cuda):
         raise ValueError("tfp8 operates on GPU tensors only (no CPU path)")
     if out.device != device:
         raise ValueError(f"tensors on different devices ({device} and {out.device})")
     if out.dtype != dtype or tuple(out.shape) != tuple(shape):
         raise ValueError(f"out must be {dtype} {list(shape)}, got {out.dtype} {list(out.shape)}")
-    return out
-
-
-def _out_rows(out: torch.Tensor) -> int:
-    """Row stride of a 2-D output whose rows are contiguous."""
-    if out.shape[0] and out.shape[1] > 1 and out.stride(1) != 1:
+    if out.numel() and shape[-1] > 1 and out.stride(-1) != 1:
         raise ValueError("the rows of out must be contiguous")
-    return out.stride(0) if out.shape[0] > 1 else out.shape[1]
+    return out, out.stride(-2) if shape[-2] > 1 else shape[-1]
 
 
 def compress_t(x: torch.Tensor, block: int = 128, target: float = 1.0, offsets=None, out=None,
@@ -554,8 +550,8 @@ def matmul(a, b, block: int = 128, dtype: torch.dtype = torch.bfloat16, out=None
     (n, kb), rb = _operand(b, block, 2, "b")
     if k != kb:
         raise ValueError(f"a and b have rows of {k} and {kb} elements")
-    out = _product_out(out, (m, n), dtype, a, b)
-    _run(out, matmul_raw, ra, rb, m, n, k, block, out.data_ptr(), dt, _out_rows(out), _stream(out))
+    out, ldc = _product_out(out, (m, n), dtype, a, b)
+    _run(out, matmul_raw, ra, rb, m, n, k, block, out.data_ptr(), dt, ldc, _stream(out))
     return out
 
 
@@ -573,9 +569,9 @@ def matmul_grouped(a, b, offsets: torch.Tensor, block: int = 128,
     groups = _offsets_of(offsets, a[0])
     if groups != g:
         raise ValueError(f"offsets cut {groups} groups and b holds {g}")
-    out = _product_out(out, (m, n), dtype, a, b)
+    out, ldc = _product_out(out, (m, n), dtype, a, b)
     _run(out, matmul_grouped_raw, ra, rb, offsets.data_ptr(), groups, m, n, k, block,
-         out.data_ptr(), dt, _out_rows(out), _stream(out))
+         out.data_ptr(), dt, ldc, _stream(out))
     return out
 
 
@@ -592,7 +588,7 @@ def matmul_grouped_t(a, b, offsets: torch.Tensor, rows: int, block: int = 128,
     kp = padded_rows(rows, groups, block)
     if k != kp or kb != kp:
         raise ValueError(f"{rows} rows in {groups} groups are {kp} elements a row, got {k} and {kb}")
-    out = _product_out(out, (groups, m, n), dtype, a, b)
+    out, _ = _product_out(out, (groups, m, n), dtype, a, b)
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")
     _run(out, matmul_grouped_t_raw, ra, rb, offsets.data_ptr(), groups, rows, m, n, block,

@@ -592,11 +592,11 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
 // 8-bit operands with one scale each reaches 3.1): 4540 cycles a step, 2048 of them the matrix
 // units', at a clock that the power limit holds near 1.9 GHz.  Codes that are all zero take 13% less
 // time at the same work, and a loop over tiles that fetches the next one's codes under the stores of
-// this one gained nothing.  16384 rows in 8 groups by 5120 x 4096: 435 to 485 us, the same rate less
+// this one gained nothing.  16384 rows in 8 groups by 5120 x 4096: 435 to 467 us, the same rate less
 // its last round of tiles, a third full.
 // float32, tiles of 256 x 128: widening the codes takes eight more vector instructions for each 16 x
 // 16 tile and step, and the matrix instructions have half the rate.  8 groups of 16384 rows in all,
-// 4096 x 2560 each: 413 to 465 us, 0.74 to 0.83 PFLOP/s; a tile is 16 steps deep there, 41 us, of which
+// 4096 x 2560 each: 413 to 460 us, 0.75 to 0.83 PFLOP/s; a tile is 16 steps deep there, 41 us, of which
 // 8.6 are its start, its first loads and its stores.  In tiles of 64 x 64 (1003 x 2571 x 2560: 25 us)
 // widening is what bounds it: 64 of a wavefront's 104 vector instructions a step, for four 16 x 16
 // tiles; larger tiles, which widen less, leave compute units without one.
