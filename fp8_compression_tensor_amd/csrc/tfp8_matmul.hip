@@ -594,12 +594,14 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
 // time at the same work, and a loop over tiles that fetches the next one's codes under the stores of
 // this one gained nothing.  16384 rows in 8 groups by 5120 x 4096: 435 to 467 us, the same rate less
 // its last round of tiles, a third full.
-// float32, tiles of 256 x 128: widening the codes takes eight more vector instructions for each 16 x
-// 16 tile and step, and the matrix instructions have half the rate.  8 groups of 16384 rows in all,
-// 4096 x 2560 each: 413 to 460 us, 0.75 to 0.83 PFLOP/s; a tile is 16 steps deep there, 41 us, of which
-// 8.6 are its start, its first loads and its stores.  In tiles of 64 x 64 (1003 x 2571 x 2560: 25 us)
-// widening is what bounds it: 64 of a wavefront's 104 vector instructions a step, for four 16 x 16
-// tiles; larger tiles, which widen less, leave compute units without one.
+// float32, tiles of 128 x 128 by four wavefronts, two workgroups a compute unit: widening the codes
+// takes eight more vector instructions for each 16 x 16 tile and step, and the matrix instructions have
+// half the rate.  8192 x 8192 x 8192: 1082 us, 1.02 PFLOP/s.  8 groups of 16384 rows in all, 4096 x 2560
+// each: 420 us, 0.82 PFLOP/s; a tile is 16 steps deep there.  (In tiles of 256 x 128 by eight wavefronts
+// 1093 and 428 us, and 6400 rows in 16 groups by 5120 x 1024 152 us, against 109.)  In tiles of 64 x
+// 64 (1003 x 2571 x 2560: 25 us) widening is what bounds it: 64 of a wavefront's 104 vector
+// instructions a step, for four 16 x 16 tiles; larger tiles, which widen less, leave compute units
+// without one.
 //
 // The kernel only calls this function: a kernel's own body is also read by the host's pass, which
 // does not know these builtins.
@@ -876,12 +878,12 @@ tfp8_status launch_tiles(void (*kernel)(ProductArgs), ProductArgs p, int64_t mt,
 }
 
 // How long a kernel takes for tiles of bm x bn (ns): `first` and `step` a step where every compute
-// unit has one workgroup, and the same where it has all `slots` that fit.  From the times of 512 products
+// unit has one workgroup, and the same where it has all `slots` that fit.  From the times of 475 products
 // of each output type, of 1 to 4096 rows and 512 to 16384 columns, 640 to 5120 deep, dense, in 4
-// to 32 groups and by groups along the depth, a fifth of them with operands that no cache holds; fitted
+// to 32 groups and by groups along the depth, a ninth of them with operands that no cache holds; fitted
 // so that the choice below costs least: what it picks takes 0.8% longer than the best of these
-// kernels on average for bfloat16 outputs, 1.1% for float32 (a choice by the number of rows alone took
-// 20% longer, up to 4 times as long).
+// kernels on average for bfloat16 outputs, 1.5% for float32 (a choice by the number of rows alone took
+// 20% longer, up to 4 times as long).  slots = 0: no such kernel.
 struct Pace {
   int bm, bn, slots;
   int64_t first, step, first_full, step_full;
@@ -894,13 +896,13 @@ constexpr Pace kPace[2][kKinds] = {{{256, 256, 1, 11410, 2320, 11410, 2320},
                                     {16, 16, 4, 3010, 17, 4290, 251},
                                     {32, 32, 2, 3670, 95, 5310, 277},
                                     {32, 48, 1, 3250, 160, 3250, 160}},
-                                   {{256, 128, 1, 9340, 1910, 9340, 1910},
-                                    {},  // 128 x 128: first in 2% of the float32 products only
-                                    {64, 64, 4, 2690, 560, 6420, 1280},
-                                    {64, 64, 2, 3660, 420, 8100, 1080},
-                                    {16, 16, 4, 2680, 30, 4910, 260},
-                                    {32, 32, 2, 3930, 107, 4980, 243},
-                                    {32, 48, 1, 3710, 153, 3710, 153}}};
+                                   {{128, 128, 2, 6570, 1200, 6870, 1780},
+                                    {},
+                                    {64, 64, 4, 2940, 550, 6420, 1230},
+                                    {64, 64, 2, 3560, 470, 8090, 1150},
+                                    {16, 16, 4, 3220, 30, 5790, 203},
+                                    {32, 32, 2, 3990, 112, 7000, 281},
+                                    {32, 48, 1, 3460, 186, 3460, 186}}};
 
 int64_t estimate(const Pace &k, int64_t tiles, int64_t steps, int64_t cus) {
   const int64_t one = k.first + steps * k.step, full = k.first_full + steps * k.step_full;
@@ -955,9 +957,8 @@ tfp8_status launch_product(const ProductArgs &p, hipStream_t st) {
     if (best == kMiddle) return run(k_matmul_tile<128, 128, 2, 4, 1, 0, MODE, F32OUT>, 512);
   if (best == kSmall) return run(k_matmul_tile<64, 64, 2, 2, 1, 16, MODE, F32OUT>, 256);
   if (best == kSmallTeams) return run(k_matmul_tile<64, 64, 2, 2, 2, 16, MODE, F32OUT>, 512);
-  return run(k_matmul_tile<256, F32OUT ? 128 : 256, F32OUT ? 4 : 2, F32OUT ? 2 : 4, 1, 0, MODE,
-                           F32OUT>,
-             512);
+  constexpr int LARGE = F32OUT ? 128 : 256, ACROSS = F32OUT ? 2 : 4;
+  return run(k_matmul_tile<LARGE, LARGE, 2, ACROSS, 1, 0, MODE, F32OUT>, 64 * 2 * ACROSS);
 }
 
 template <int MODE>

@@ -2,8 +2,7 @@
 
 A product goes to the kernel whose rounds of workgroups are estimated to be done first, so that each
 appears only at sizes of its own.  The comment on each case names what an MI355X (256 compute units)
-takes for it, bfloat16 / float32: `256` the tiles of 256 rows, `128` and `64` those of 128 x 128 and
-64 x 64, `64+` the last with two teams, `few16`, `few32`, `few48` the kernels for few rows by their
+takes for it, bfloat16 / float32: `256`, `128` and `64` the tiles of so many rows and columns, `64+` the last with two teams, `few16`, `few32`, `few48` the kernels for few rows by their
 columns.  On another number of compute units the cases stay right and reach other kernels."""
 import numpy as np
 import pytest
@@ -43,19 +42,19 @@ def assert_frame(buf, out, what):
     (33, 4200, 4608, 512),    # few32 / few32
     (28, 10300, 2560, 256),   # few48 / few48
     (20, 11000, 8448, 128),   # few48 / few48, refilled
-    (90, 9000, 2176, 128),    # 64+ / 64+, the teams' steps uneven, 17 blocks: refilled
-    (200, 2600, 4352, 256),   # 64+ / few48, refilled
+    (90, 9000, 2176, 128),    # 64+ / 64, the teams' steps uneven, 17 blocks: refilled
+    (200, 2600, 4352, 256),   # 64+ / 64+, refilled
     (130, 4200, 4608, 512),   # 64+ / few48
     (777, 2561, 2176, 128),   # 64 / 64, refilled
     (777, 2561, 2560, 512),   # 64 / 64
-    (1537, 2561, 1152, 128),  # 128 / 64
-    (1537, 2561, 2560, 256),  # 128 / 64
-    (2100, 4100, 1152, 128),  # 256 / 64
-    (2300, 4100, 1280, 256),  # 256 / 64
-    (2300, 4100, 1536, 512),  # 256 / 64
-    (4100, 4300, 640, 128),   # 128 / 256
-    (4100, 4300, 1280, 256),  # 128 / 256
-    (4100, 4300, 1536, 512),  # 128 / 256
+    (1537, 2561, 1152, 128),  # 128 / 128
+    (1537, 2561, 2560, 256),  # 128 / 128
+    (2100, 4100, 1152, 128),  # 256 / 128
+    (2300, 4100, 1280, 256),  # 256 / 128
+    (2300, 4100, 1536, 512),  # 256 / 128
+    (4100, 4300, 640, 128),   # 128 / 128
+    (4100, 4300, 1280, 256),  # 128 / 128
+    (4100, 4300, 1536, 512),  # 128 / 128
 ])
 def test_matmul_in_every_kernel(m, n, k, block, dt):
     say(f"matmul {m}x{n}x{k} block {block} {dt}")
@@ -71,14 +70,16 @@ def test_matmul_in_every_kernel(m, n, k, block, dt):
 @pytest.mark.parametrize("dt", DTYPES)
 @pytest.mark.parametrize("counts,n,k,block", [
     ([10, 0, 20], 1000, 8448, 128),            # few16 / few16, refilled
-    ([14, 0, 9], 5100, 8448, 128),             # few16 / few32, refilled
-    ([100, 1, 159], 1000, 2176, 128),          # few32 / few32
+    ([14, 0, 9], 5100, 8448, 128),             # few16 / few16, refilled
+    ([100, 1, 159], 1000, 2176, 128),          # few32 / few48
+    ([20, 12, 30], 5000, 8448, 128),           # few32 / few32, refilled
+    ([33], 9000, 1024, 256),                   # few48 / few48
     ([40] * 5, 2305, 8448, 128),               # 64+ / few48, refilled
     ([100, 1, 159], 3000, 2176, 128),          # 64+ / 64+
     ([300, 0, 777, 1, 500], 1793, 2176, 128),  # 64 / 64, refilled
-    ([300, 0, 777, 1, 500], 2561, 1536, 512),  # 128 / 64
-    ([2100, 0, 3, 400], 2561, 1152, 128),      # 128 / 256
-    ([2100, 0, 3, 400], 4100, 1280, 256),      # 256 / 64
+    ([300, 0, 777, 1, 500], 2561, 1536, 512),  # 128 / 128
+    ([2100, 0, 3, 400], 2561, 1152, 128),      # 128 / 128
+    ([2100, 0, 3, 400], 4100, 1280, 256),      # 256 / 128
     ([1] * 200 + [0] * 60 + [300, 2], 300, 384, 128),  # more groups than a wavefront has lanes
 ])
 def test_matmul_grouped_in_every_kernel(counts, n, k, block, dt):
@@ -102,9 +103,9 @@ def test_matmul_grouped_in_every_kernel(counts, n, k, block, dt):
     ([2500], 260, 1793, 128),                       # 64+ / 64+, refilled
     ([2200, 0, 2100], 260, 2561, 128),              # 64 / 64, refilled
     ([0, 1000, 793], 520, 2049, 256),               # 64 / 64
-    ([300, 0, 777, 1, 500], 260, 3001, 512),        # 128 / 64
-    ([300, 0, 777, 1, 500], 520, 2049, 128),        # 128 / 256
-    ([300, 0, 777, 1, 500], 2050, 2561, 128),       # 256 / 256
+    ([300, 0, 777, 1, 500], 260, 3001, 512),        # 128 / 128
+    ([300, 0, 777, 1, 500], 520, 2049, 128),        # 128 / 128
+    ([300, 0, 777, 1, 500], 2050, 2561, 128),       # 256 / 128
 ])
 def test_matmul_grouped_t_in_every_kernel(counts, m, n, block, dt):
     say(f"matmul_grouped_t {counts}, {m}x{n} block {block} {dt}")
