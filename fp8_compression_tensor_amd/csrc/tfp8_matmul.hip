@@ -868,15 +868,6 @@ using namespace tfp8;
 
 bool product_block_ok(int32_t block) { return block == 128 || block == 256 || block == 512; }
 
-// Launches `kernel` with one workgroup for each of mt x nt tiles (times `times`).
-tfp8_status launch_tiles(void (*kernel)(ProductArgs), ProductArgs p, int64_t mt, int64_t nt,
-                         int64_t times, int threads, hipStream_t st) {
-  if (mt * nt > (((int64_t)1 << 32) - 1) / threads / times) return TFP8_E_SIZE;
-  p.mtiles = (int32_t)mt;
-  p.ntiles = (int32_t)nt;
-  return launch(kernel, (unsigned)(mt * nt * times), threads, st, p);
-}
-
 // How long a kernel takes for tiles of bm x bn (ns): `first` and `step` a step where every compute
 // unit has one workgroup, and the same where it has all `slots` that fit.  From the times of 475 products
 // of each output type, of 1 to 4096 rows and 512 to 16384 columns, 640 to 5120 deep, dense, in 4
@@ -885,24 +876,24 @@ tfp8_status launch_tiles(void (*kernel)(ProductArgs), ProductArgs p, int64_t mt,
 // kernels on average for bfloat16 outputs, 1.5% for float32 (a choice by the number of rows alone took
 // 20% longer, up to 4 times as long).  slots = 0: no such kernel.
 struct Pace {
-  int bm, bn, slots;
+  int bm, bn, threads, slots;
   int64_t first, step, first_full, step_full;
 };
 enum : int { kLarge, kMiddle, kSmall, kSmallTeams, kFew, kFew32, kFew48, kKinds };
-constexpr Pace kPace[2][kKinds] = {{{256, 256, 1, 11410, 2320, 11410, 2320},
-                                    {128, 128, 2, 3590, 1310, 5590, 1450},
-                                    {64, 64, 4, 2330, 460, 4230, 1290},
-                                    {64, 64, 2, 3080, 360, 4610, 690},
-                                    {16, 16, 4, 3010, 17, 4290, 251},
-                                    {32, 32, 2, 3670, 95, 5310, 277},
-                                    {32, 48, 1, 3250, 160, 3250, 160}},
-                                   {{128, 128, 2, 6570, 1200, 6870, 1780},
+constexpr Pace kPace[2][kKinds] = {{{256, 256, 512, 1, 11410, 2320, 11410, 2320},
+                                    {128, 128, 512, 2, 3590, 1310, 5590, 1450},
+                                    {64, 64, 256, 4, 2330, 460, 4230, 1290},
+                                    {64, 64, 512, 2, 3080, 360, 4610, 690},
+                                    {16, 16, 512, 4, 3010, 17, 4290, 251},
+                                    {32, 32, 512, 2, 3670, 95, 5310, 277},
+                                    {32, 48, 512, 1, 3250, 160, 3250, 160}},
+                                   {{128, 128, 256, 2, 6570, 1200, 6870, 1780},
                                     {},
-                                    {64, 64, 4, 2940, 550, 6420, 1230},
-                                    {64, 64, 2, 3560, 470, 8090, 1150},
-                                    {16, 16, 4, 3220, 30, 5790, 203},
-                                    {32, 32, 2, 3990, 112, 7000, 281},
-                                    {32, 48, 1, 3460, 186, 3460, 186}}};
+                                    {64, 64, 256, 4, 2940, 550, 6420, 1230},
+                                    {64, 64, 512, 2, 3560, 470, 8090, 1150},
+                                    {16, 16, 512, 4, 3220, 30, 5790, 203},
+                                    {32, 32, 512, 2, 3990, 112, 7000, 281},
+                                    {32, 48, 512, 1, 3460, 186, 3460, 186}}};
 
 int64_t estimate(const Pace &k, int64_t tiles, int64_t steps, int64_t cus) {
   const int64_t one = k.first + steps * k.step, full = k.first_full + steps * k.step_full;
@@ -919,46 +910,51 @@ int64_t estimate(const Pace &k, int64_t tiles, int64_t steps, int64_t cus) {
 // ones leave less over at the edges and in the last round, two teams halve the steps of a product
 // with few tiles, and the kernels for few rows divide them by eight.
 template <int MODE, bool F32OUT>
-tfp8_status launch_product(const ProductArgs &p, hipStream_t st) {
+tfp8_status launch_product(ProductArgs p, hipStream_t st) {
   const int64_t times = MODE == kGroupedDepth ? p.groups : 1, cus = cu_count();
   const int64_t m = p.m, n = p.n;
   const int64_t steps =
       MODE == kGroupedDepth ? ((int64_t)p.rows / p.groups + kStep - 1) / kStep : p.steps;
   int best = -1;
-  int64_t least = 0;
+  int64_t least = 0, grid = 0;
   for (int i = 0; i < (MODE == kGroupedDepth ? kFew : kKinds); ++i) {
     const Pace &k = kPace[F32OUT][i];
     if (k.slots == 0) continue;
-    int64_t mt = (m + k.bm - 1) / k.bm;
-    if (MODE == kGroupedRows) {  // a tile for each group, and half of one more on average
-      const int64_t least_mt = m < p.groups ? m : p.groups;
+    const int64_t nt = (n + k.bn - 1) / k.bn;
+    int64_t mt = (m + k.bm - 1) / k.bm, most = mt;
+    if (MODE == kGroupedRows) {
+      // as a rule a tile for each group, and half of one more on average; at most as many as
+      // groups of any sizes come to, with the rows past the last as one more group
+      const int64_t some = m < p.groups ? m : p.groups, all = m <= p.groups ? m : p.groups + 1;
       mt = m / k.bm + p.groups / 2;
-      mt = mt < least_mt ? least_mt : mt;
+      mt = mt < some ? some : mt;
+      most = (m + all * (k.bm - 1)) / k.bm;
     }
-    const int64_t ns = estimate(k, mt * ((n + k.bn - 1) / k.bn) * times, steps, cus);
+    if (most * nt > (((int64_t)1 << 32) - 1) / k.threads / times) continue;  // HIP's limit
+    const int64_t ns = estimate(k, mt * nt * times, steps, cus);
     if (best < 0 || ns < least) {
       best = i;
       least = ns;
+      p.mtiles = (int32_t)most;
+      p.ntiles = (int32_t)nt;
+      grid = most * nt * times;
     }
   }
-  const int bm = kPace[F32OUT][best].bm, bn = kPace[F32OUT][best].bn;
-  const auto run = [&](void (*kernel)(ProductArgs), int threads) {
-    // the tiles that groups of any sizes can come to, with the rows past the last as one more group
-    const int64_t mt = MODE == kGroupedRows ? (m + (int64_t)(p.groups + 1) * (bm - 1)) / bm
-                                            : (m + bm - 1) / bm;
-    return launch_tiles(kernel, p, mt, (n + bn - 1) / bn, times, threads, st);
+  if (best < 0) return TFP8_E_SIZE;
+  const auto run = [&](void (*kernel)(ProductArgs)) {
+    return launch(kernel, (unsigned)grid, kPace[F32OUT][best].threads, st, p);
   };
   if constexpr (MODE != kGroupedDepth) {
-    if (best == kFew) return run(k_matmul_split<1, 1, MODE, F32OUT>, 512);
-    if (best == kFew32) return run(k_matmul_split<2, 2, MODE, F32OUT>, 512);
-    if (best == kFew48) return run(k_matmul_split<2, 3, MODE, F32OUT>, 512);
+    if (best == kFew) return run(k_matmul_split<1, 1, MODE, F32OUT>);
+    if (best == kFew32) return run(k_matmul_split<2, 2, MODE, F32OUT>);
+    if (best == kFew48) return run(k_matmul_split<2, 3, MODE, F32OUT>);
   }
   if constexpr (!F32OUT)
-    if (best == kMiddle) return run(k_matmul_tile<128, 128, 2, 4, 1, 0, MODE, F32OUT>, 512);
-  if (best == kSmall) return run(k_matmul_tile<64, 64, 2, 2, 1, 16, MODE, F32OUT>, 256);
-  if (best == kSmallTeams) return run(k_matmul_tile<64, 64, 2, 2, 2, 16, MODE, F32OUT>, 512);
-  constexpr int LARGE = F32OUT ? 128 : 256, ACROSS = F32OUT ? 2 : 4;
-  return run(k_matmul_tile<LARGE, LARGE, 2, ACROSS, 1, 0, MODE, F32OUT>, 64 * 2 * ACROSS);
+    if (best == kMiddle) return run(k_matmul_tile<128, 128, 2, 4, 1, 0, MODE, F32OUT>);
+  if (best == kSmall) return run(k_matmul_tile<64, 64, 2, 2, 1, 16, MODE, F32OUT>);
+  if (best == kSmallTeams) return run(k_matmul_tile<64, 64, 2, 2, 2, 16, MODE, F32OUT>);
+  constexpr int LARGE = F32OUT ? 128 : 256;
+  return run(k_matmul_tile<LARGE, LARGE, 2, F32OUT ? 2 : 4, 1, 0, MODE, F32OUT>);
 }
 
 template <int MODE>

@@ -133,3 +133,23 @@ def test_large_products_repeat_bit_for_bit(m, n, k):
     for dtype in DTYPES.values():
         first = tfp8.matmul(a, b, 128, dtype)
         assert all(torch.equal(first, tfp8.matmul(a, b, 128, dtype)) for _ in range(3))
+
+
+@pytest.mark.parametrize("rows,groups,used", [(3, 200, 2), (40, 40, 40), (41, 40, 30), (100, 5000, 60)])
+def test_matmul_grouped_with_more_groups_than_tiles_of_rows(rows, groups, used):
+    """One row to each of `used` groups spread over all of them, the rest past the last group."""
+    say(f"matmul_grouped {rows} rows, {used} of {groups} groups with one")
+    n, k, block = 48, 256, 128
+    rng = np.random.default_rng(groups)
+    counts = np.zeros(groups, np.int64)
+    counts[np.sort(rng.choice(groups, used, replace=False))] = 1
+    off = offsets_of(counts)
+    a, w = random_operand(rows, k, block, rng), random_operand(groups * n, k, block, rng)
+    av, wv = rotated_values(a, block), rotated_values(w, block).reshape(groups, n, k)
+    rep = np.repeat(np.arange(groups), counts)
+    wg = tuple(t.view(groups, n, -1) for t in to_gpu(w))
+    out = torch.full((rows, n), 7.0, device=DEV)
+    tfp8.matmul_grouped(to_gpu(a), wg, torch.from_numpy(off).to(DEV), block, torch.float32, out=out)
+    parts = [exact_on_gpu(av[i:i + 1], wv[g]) for i, g in enumerate(rep)]
+    assert_product(out[:used], tuple(np.concatenate(t) for t in zip(*parts)), k, "groups of one row")
+    assert not out[used:].any()
