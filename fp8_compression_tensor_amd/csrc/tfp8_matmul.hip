@@ -588,20 +588,20 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
 //
 // What bounds it.  bfloat16, tiles of 256 x 256: a matrix instruction takes 32 cycles of its unit, and
 // with the eight vector instructions of its scaled addition 48 of its SIMD.  8192 x 16384 x 4096 in
-// blocks of 256 takes 560 to 620 us on different cards, 1.77 to 1.96 PFLOP/s (a library product of
+// blocks of 256 takes 560 to 645 us on different cards, 1.7 to 1.96 PFLOP/s (a library product of
 // 8-bit operands with one scale each reaches 3.1): 4540 cycles a step, 2048 of them the matrix
 // units', at a clock that the power limit holds near 1.9 GHz.  Codes that are all zero take 13% less
 // time at the same work, and a loop over tiles that fetches the next one's codes under the stores of
-// this one gained nothing.  16384 rows in 8 groups by 5120 x 4096: 435 to 467 us, the same rate less
+// this one gained nothing.  16384 rows in 8 groups by 5120 x 4096: 435 to 480 us, the same rate less
 // its last round of tiles, a third full.
 // float32, tiles of 128 x 128 by four wavefronts, two workgroups a compute unit: widening the codes
-// takes eight more vector instructions for each 16 x 16 tile and step, and the matrix instructions have
-// half the rate.  8192 x 8192 x 8192: 1082 us, 1.02 PFLOP/s.  8 groups of 16384 rows in all, 4096 x 2560
-// each: 420 us, 0.82 PFLOP/s; a tile is 16 steps deep there.  (In tiles of 256 x 128 by eight wavefronts
-// 1093 and 428 us, and 6400 rows in 16 groups by 5120 x 1024 152 us, against 109.)  In tiles of 64 x
-// 64 (1003 x 2571 x 2560: 25 us) widening is what bounds it: 64 of a wavefront's 104 vector
-// instructions a step, for four 16 x 16 tiles; larger tiles, which widen less, leave compute units
-// without one.
+// takes eight more vector instructions for each 16 x 16 tile and step, and the matrix instructions
+// have half the rate.  8192 x 8192 x 8192: 1082 us, 1.02 PFLOP/s.  8 groups of 16384 rows in all,
+// 4096 x 2560 each: 403 to 465 us, 0.74 to 0.85 PFLOP/s; a tile is 16 steps deep there.  (In tiles
+// of 256 x 128 by eight wavefronts 1093 us, and 428 where this takes 420; 6400 rows in 16 groups by
+// 5120 x 1024 152 us, against 109.)  In tiles of 64 x 64 (1003 x 2571 x 2560: 25 us) widening is
+// what bounds it: 64 of a wavefront's 104 vector instructions a step, for four 16 x 16 tiles;
+// larger tiles, which widen less, leave compute units without one.
 //
 // The kernel only calls this function: a kernel's own body is also read by the host's pass, which
 // does not know these builtins.
