@@ -501,9 +501,10 @@ def compress_t(x: torch.Tensor, block: int = 128, target: float = 1.0, offsets=N
     (codes uint8 [cols, kp], alpha, scale float32 [cols, kp / block]) whose blocks run along the
     rows of x, for products that contract over them.
 
-    offsets (int64 [groups + 1] on the GPU, offsets[0] = 0, ascending) cuts the rows into groups;
-    each group starts at a multiple of the block in the output, kp = padded_rows(rows, groups,
-    block), and what no row fills counts as zeros.  flags: 0 or FLAG_NO_ROTATION."""
+    offsets (int64 [groups + 1] on the GPU, ascending) cuts the rows into groups, [offsets[g],
+    offsets[g + 1]); each group starts at a multiple of the block in the output, kp =
+    padded_rows(rows, groups, block), what no row fills counts as zeros, and rows before offsets[0]
+    or past offsets[-1] are left out.  flags: 0 or FLAG_NO_ROTATION."""
     if not (isinstance(x, torch.Tensor) and x.is_cuda):
         raise ValueError("tfp8 operates on GPU tensors only (no CPU path)")
     if x.dim() != 2:
@@ -559,7 +560,7 @@ def matmul_grouped(a, b, offsets: torch.Tensor, block: int = 128,
                    dtype: torch.dtype = torch.bfloat16, out=None):
     """Rows grouped by expert: a = (codes [m, k], ...) with the rows of group g at
     [offsets[g], offsets[g + 1]), b = (codes [groups, n, k], ...) -> [m, n], each row times its
-    group's b.  Rows past offsets[-1] become zeros."""
+    group's b.  Rows before offsets[0] and past offsets[-1] become zeros."""
     _product_block(block)
     dt = _out_dtype(dtype)
     (m, k), ra = _operand(a, block, 2, "a")

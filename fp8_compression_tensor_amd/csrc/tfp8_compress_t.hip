@@ -99,7 +99,7 @@ __global__ __launch_bounds__(256) void k_compress_t(TransposeArgs p) {
   int rows = 0;
   if (kb < p.blocks) {
     if (p.offsets) {
-      const GroupTile g = tile_of_groups(p.offsets, p.groups, p.rows, B, p.groups - 1,
+      const GroupTile g = tile_of_groups(p.offsets, p.groups, p.rows, B, false,
                                          [&](int64_t) { return kb; });
       row0 = g.row0;
       rows = g.rows;

@@ -254,17 +254,16 @@ __device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
     // that there are (3200 rows in 16 groups by 2560 x 2048: 43 us, against 83 in parts of the launch,
     // which left the last XCD without work)
     const GroupTile g =
-        tile_of_groups(p.offsets, p.groups, p.m, BM, p.groups, [&](int64_t there) -> int64_t {
-          const int mtiles = there < p.mtiles ? (int)there : p.mtiles;  // more: overlapping groups
-          const uint32_t all = (uint32_t)mtiles * p.ntiles, at = place_of_workgroup(all);
+        tile_of_groups(p.offsets, p.groups, p.m, BM, true, [&](int64_t there) -> int64_t {
+          const uint32_t all = (uint32_t)there * p.ntiles, at = place_of_workgroup(all);
           if (at >= all) return there;
-          tile_at(at, mtiles, p.ntiles, mt, nt);
+          tile_at(at, (int)there, p.ntiles, mt, nt);
           return mt;
         });
     if (g.rows <= 0) return false;
     m0 = g.row0;
     t.mv = g.rows;
-    if (g.group == p.groups) {  // rows past the last group: zeros
+    if (g.group < 0) {  // rows of no group: zeros
       s1 = 0;
     } else {
       bskip = (int64_t)g.group * p.n * p.b.ld;
@@ -924,8 +923,8 @@ tfp8_status launch_product(ProductArgs p, hipStream_t st) {
     int64_t mt = (m + k.bm - 1) / k.bm, most = mt;
     if (MODE == kGroupedRows) {
       // as a rule a tile for each group, and half of one more on average; at most as many as
-      // groups of any sizes come to, with the rows past the last as one more group
-      const int64_t some = m < p.groups ? m : p.groups, all = m <= p.groups ? m : p.groups + 1;
+      // groups of any sizes come to, with the rows before the first and past the last as two more
+      const int64_t some = m < p.groups ? m : p.groups, all = m < p.groups + 2 ? m : p.groups + 2;
       mt = m / k.bm + p.groups / 2;
       mt = mt < some ? some : mt;
       most = (m + all * (k.bm - 1)) / k.bm;

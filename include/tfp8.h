@@ -190,9 +190,11 @@ tfp8_status tfp8_accumulate(const uint8_t *codes, const float *alpha, const floa
  * with k = 0 it writes zeros.
  *
  * Groups.  offsets[groups + 1] (device memory, int64) cuts `rows` rows sorted by group: group g has
- * rows [offsets[g], offsets[g + 1]), offsets[0] = 0, not descending, offsets[groups] <= rows.  A
- * group may be empty.  Offsets are clamped to these rules' bounds on the device, so others give
- * wrong values and no access outside the buffers.  1 <= groups <= TFP8_MAX_GROUPS (TFP8_E_ARG). */
+ * rows [offsets[g], offsets[g + 1]), not descending.  A group may be empty, and rows before
+ * offsets[0] and from offsets[groups] on are of no group.  On the device an offset is taken as clamped
+ * to [0, rows] and to the largest one before it, so that whatever the offsets hold, groups do
+ * not overlap and nothing outside the buffers is accessed.  1 <= groups <= TFP8_MAX_GROUPS
+ * (TFP8_E_ARG). */
 #define TFP8_MAX_GROUPS 65536
 
 /* Length of a row that holds `rows` rows sorted into `groups` groups, each group rounded up to a
@@ -205,7 +207,7 @@ int64_t tfp8_padded_rows(int64_t rows, int32_t groups, int32_t block);
  * codes[cols][kp], alpha and scale[cols][kp / block], the operand of a product whose contraction
  * runs over the rows.  Rows past the end of a group's last block count as zeros; blocks past the
  * last group's are written as zero blocks.  offsets = NULL with groups = 1: all rows are one group.
- * Rows past offsets[groups] are left out.  flags: 0 or TFP8_FLAG_NO_ROTATION (TFP8_E_ARG: no
+ * Rows of no group are left out.  flags: 0 or TFP8_FLAG_NO_ROTATION (TFP8_E_ARG: no
  * product takes INT8 codes).  x is aligned to its elements; rows may start at any of them.
  * rows * ldx and cols * kp are at most TFP8_MAX_N (TFP8_E_SIZE). */
 tfp8_status tfp8_compress_t(const void *x, tfp8_dtype x_dtype, int64_t rows, int64_t cols,
@@ -223,7 +225,7 @@ tfp8_status tfp8_matmul(const uint8_t *a_codes, int64_t a_ld, const float *a_alp
 
 /* Grouped by rows: B[groups][n][k] holds one operand per group, one after the other (row r of group
  * g at row g * n + r; groups * n <= 2^31 - 1), and each row of A[m][k] takes its group's:
- * out[r] = A^[r] B^[g(r)]^T.  Rows past offsets[groups] become zeros. */
+ * out[r] = A^[r] B^[g(r)]^T.  Rows of no group become zeros. */
 tfp8_status tfp8_matmul_grouped(const uint8_t *a_codes, int64_t a_ld, const float *a_alpha,
                                 const float *a_scale, int64_t a_lds, const uint8_t *b_codes,
                                 int64_t b_ld, const float *b_alpha, const float *b_scale,
