@@ -7,7 +7,8 @@
 // rotation a^ = u_a).  H / sqrt(B) is orthogonal: a^ . b^ = u_a . u_b, and
 //   C[m][n] = sum over blocks of r_a[m] r_b[n] sum_k dec(qa[m][k]) dec(qb[n][k]).
 // The inner sum is what the matrix cores compute on the codes as they are; no Hadamard, no
-// decompressed copy.  Each 128-deep partial tile is scaled by r_a r_b and added in float32.
+// decompressed copy.  Each 128-deep partial tile is scaled by r_a r_b and added in float32 (float64
+// where r_a r_b may leave its range).
 #include <math.h>
 #include <stdint.h>
 
@@ -125,6 +126,10 @@ __device__ __forceinline__ i32x4 buffer_of(const void *base, int bytes) {
   return i32x4{__builtin_amdgcn_readfirstlane((int)p),
                __builtin_amdgcn_readfirstlane((int)(p >> 32) & 0xFFFF),
                __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
+}
+
+__device__ __forceinline__ const uint8_t *base_of(i32x4 buffer) {
+  return (const uint8_t *)((uint64_t)(uint32_t)buffer[0] | (uint64_t)(uint32_t)buffer[1] << 32);
 }
 
 // 16 bytes a lane from the buffer at offset voff + soff to LDS, lane l's at to + 16 l.  Written as
@@ -301,6 +306,42 @@ __device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
   return true;
 }
 
+// Which ranges the factors r = s / alpha of an operand come from.  r_a r_b is one float32 factor of a
+// block's sum.  An r below float32's normal range (blocks of values below about 2^-115) has lost
+// bits, which is below 2^-123 of a result for each kStep codes as long as the other operand's r is
+// at most 1.  A tile where an r of one operand may be so small (alpha above 2^84: every r below 2^-126
+// has one, whatever its target) and one of the other above 1 is computed again by wide_range_tile.
+enum : int { kTinyA = 1, kLargeA = 2, kTinyB = 4, kLargeB = 8 };
+
+// Notes four blocks of a row of each lane, the rows all of A or all of B; as integers, which order like
+// these positive floats.  Noting and asking at the end take 1% of a large product, 0.2 us of one of
+// few rows.
+__device__ __forceinline__ void note_range(const f32x4 s, const f32x4 alpha, bool is_a, int &saw) {
+  int a[4], most = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = __float_as_int(alpha[i]);
+    most = max(most, __float_as_int(s[i]));
+  }
+  const uint64_t tiny = __ballot(max(max(a[0], a[1]), max(a[2], a[3])) > __float_as_int(0x1p84f));
+  const uint64_t large = __ballot(most > min(min(a[0], a[1]), min(a[2], a[3])));
+  if (__builtin_expect((tiny | large) != 0, 0))
+    saw |= (tiny ? (is_a ? kTinyA : kTinyB) : 0) | (large ? (is_a ? kLargeA : kLargeB) : 0);
+}
+
+// A wavefront's `saw` to its word of LDS, and, after a barrier, a wavefront's word to each lane and
+// whether together they ask for wide_range_tile.
+__device__ __forceinline__ void tell(float *words, int w, int saw) { words[w] = __int_as_float(saw); }
+template <int WAVES>
+__device__ __forceinline__ int told(const float *words) {
+  return __float_as_int(words[threadIdx.x & (WAVES - 1)]);
+}
+__device__ __forceinline__ bool wide_range(int word) {
+  if (__builtin_expect(__ballot(word) == 0, 1)) return false;
+  return (__ballot(word & kTinyA) && __ballot(word & kLargeB)) ||
+         (__ballot(word & kTinyB) && __ballot(word & kLargeA));
+}
+
 // LDS of a tile: two stages of a step's codes, A's rows then B's (four measured no
 // faster, and halve what fits), and scales r: those of a step for each stage, or (CHUNK > 0) those of
 // CHUNK blocks.  KS > 1: the workgroup's wavefronts form KS teams with stages of their own, and team
@@ -325,6 +366,7 @@ struct Feed {
 
   STAGES &lds;
   int team, w, shift, first, blocks;  // w: the wavefront within its team
+  int saw = 0;                        // of note_range
   i32x4 ra[LA], rb[LB];
   int va, vb;
   const char *sp[SC], *ap[SC];  // a wavefront's rows are of one operand
@@ -414,6 +456,7 @@ struct Feed {
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
       const int at = (int)threadIdx.x + i * ALL, row = at / QUADS, k = at % QUADS * 4;
+      note_range(x[i], y[i], (i * ALL + (team * NW + w) * 64) / QUADS < BM, saw);
 #pragma unroll
       for (int u = 0; u < 4; ++u) lds.r[k + u][row] = x[i][u] * __builtin_amdgcn_rcpf(y[i][u]);
     }
@@ -446,6 +489,7 @@ struct Feed {
     const int k = ((s >> shift) - first) & 3;
 #pragma unroll
     for (int i = 0; i < SC; ++i) {
+      if (k == 0) note_range(sv[i], av[i], w * 64 + i * NT < BM, saw);
       const float x = k & 2 ? (k & 1 ? sv[i][3] : sv[i][2]) : (k & 1 ? sv[i][1] : sv[i][0]);
       const float y = k & 2 ? (k & 1 ? av[i][3] : av[i][2]) : (k & 1 ? av[i][1] : av[i][0]);
       const int row = (int)threadIdx.x + i * NT;
@@ -583,6 +627,49 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
   if (KS > 1) wait_loads();  // no load may arrive after the workgroup has given its LDS back
 }
 
+// A tile once more, where the product of two r need not be a float32 (note_range): the factors and
+// the sums over steps in float64.  A wavefront takes one tile of 16 x 16 after the other, its codes
+// and scales straight from memory, rows past the end those of the last row again.  The kernel's
+// arguments are read again, so that no registers keep them through the loops for this.  4096 x 4096 x
+// 4096 takes 1.5 ms where every tile comes to this, 64 x 5120 x 5120 55 us.
+template <bool F32OUT, int WAVES>
+__device__ __forceinline__ void wide_range_tile(const Job &t) {
+  auto *args = __builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(args));
+  ProductArgs p;
+  __builtin_memcpy(&p, (const void *)args, sizeof p);
+  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+  const int across = (t.nv + 15) / 16, tiles = (t.mv + 15) / 16 * across;
+  const auto load = [&](const uint8_t *codes) {
+    const u32x4 lo = *(const u32x4 *)(codes + 16 * q), hi = *(const u32x4 *)(codes + 16 * q + 64);
+    return make_fragment<F32OUT>(lo, hi);
+  };
+  const auto factor = [](const float *scale, const float *alpha, int at) {
+    return (double)scale[at] * (double)__builtin_amdgcn_rcpf(alpha[at]);
+  };
+  for (int at = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); at < tiles; at += WAVES) {
+    const int row = at / across * 16 + l16, c0 = at % across * 16, col = c0 + 4 * q;
+    const int r = row < t.mv ? row : t.mv - 1;
+    const int c = c0 + l16 < t.nv ? c0 + l16 : t.nv - 1;
+    double sum[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int s = t.s0; s < t.s1; ++s) {
+      const Fragment<F32OUT> fa = load(t.ac + r * p.a.ld + s * kStep);  // offsets below 2^31
+      const Fragment<F32OUT> fb[1] = {load(t.bc + c * p.b.ld + s * kStep)};
+      f32x4 part[1];
+      mfma_row(part, fb, fa);
+      const int b = s >> p.shift;
+      const double ra = factor(t.as, t.aa, r * p.a.lds + b);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int ck = col + k < t.nv ? col + k : t.nv - 1;
+        sum[k] += (double)part[0][k] * (ra * factor(t.bs, t.ba, ck * p.b.lds + b));
+      }
+    }
+    const f32x4 v = {(float)sum[0], (float)sum[1], (float)sum[2], (float)sum[3]};
+    if (row < t.mv) store_values<F32OUT>(t.out, row * p.ldc + col, v, t.nv - col);
+  }
+}
+
 // One tile of BM x BN by WM x WN wavefronts (of KS teams).
 //
 // What bounds it.  bfloat16, tiles of 256 x 256: a matrix instruction takes 32 cycles of its unit, and
@@ -623,6 +710,11 @@ __device__ __forceinline__ void matmul_tile(const ProductArgs &p) {
   if (t.s0 < t.s1) {
     Feed<STAGES, WM * WN> feed(lds, p, t);
     run_steps<TM, TN, F32OUT>(lds, feed, p, t, mrow, nrow, acc);
+    // what other wavefronts still read of the scales is of a step past the end, and not used
+    tell(&lds.r[0][0], all, feed.saw);
+    lds_barrier();
+    if (__builtin_expect(wide_range(told<WM * WN * KS>(&lds.r[0][0])), 0))
+      return wide_range_tile<F32OUT, WM * WN * KS>(t);
   }
   // row of tiles i of this wavefront
   const auto store_row = [&](int i, const f32x4 (&v)[TN]) {
@@ -753,6 +845,7 @@ __device__ __forceinline__ void matmul_split(const ProductArgs &p) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int blocks = (int)(p.steps >> p.shift);
+  int saw = 0;  // of note_range
 
   for (int c0 = t.s0; c0 < t.s1; c0 += kSplitBlocks << p.shift) {
     // this wavefront's share of the steps whose scales fit
@@ -792,6 +885,7 @@ __device__ __forceinline__ void matmul_split(const ProductArgs &p) {
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
       const int at = tid + i * NT, row = at / QUADS, k = at % QUADS * 4;
+      note_range(x[i], y[i], (i * NT + w * 64) / QUADS < BM, saw);
       if (ROWS * QUADS % NT == 0 || row < ROWS)
 #pragma unroll
         for (int u = 0; u < 4; ++u) lds.r[k + u][row] = x[i][u] * __builtin_amdgcn_rcpf(y[i][u]);
@@ -840,16 +934,27 @@ __device__ __forceinline__ void matmul_split(const ProductArgs &p) {
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) lds.sum[w][i * TN + j][lane] = acc[i][j];
+  tell(&lds.r[0][0], w, saw);
   __syncthreads();
-  for (int at = w; at < MT * TN; at += kSplitWaves) {
-    f32x4 v = lds.sum[0][at][lane];
+  static_assert(MT * TN <= kSplitWaves, "a 16 x 16 tile a wavefront");
+  const int word = told<kSplitWaves>(&lds.r[0][0]);
+  f32x4 v;
+  if (w < MT * TN) {
+    v = lds.sum[0][w][lane];
 #pragma unroll
     for (int k = 1; k < kSplitWaves; ++k) {
-      const f32x4 o = lds.sum[k][at][lane];
+      const f32x4 o = lds.sum[k][w][lane];
 #pragma unroll
       for (int c = 0; c < 4; ++c) v[c] += o[c];
     }
-    const int row = at / TN * 16 + l16, col = at % TN * 16 + 4 * q;
+  }
+  if (__builtin_expect(wide_range(word), 0)) {
+    t.ac = base_of(from[0]);  // two pointers fewer to keep through the loop
+    t.bc = base_of(from[BM / 8]);
+    return wide_range_tile<F32OUT, kSplitWaves>(t);
+  }
+  if (w < MT * TN) {
+    const int row = w / TN * 16 + l16, col = w % TN * 16 + 4 * q;
     if (row < t.mv) store_values<F32OUT>(t.out, row * p.ldc + col, v, t.nv - col);
   }
 }
