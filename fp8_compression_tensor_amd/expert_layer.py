@@ -23,6 +23,7 @@ import sys
 import time
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (accumulate, compress, compress_t, decompress, matmul, matmul_grouped,
                matmul_grouped_t)
@@ -59,6 +60,7 @@ class ExpertLinear(torch.autograd.Function):
         return matmul_grouped((codes, alpha, scale), compressed.rows, offsets, block, x.dtype)
 
     @staticmethod
+    @once_differentiable  # the products record no graph: a second derivative is refused, not dropped
     def backward(ctx, dy):
         x, offsets = ctx.saved_tensors
         w, block = ctx.compressed, ctx.compressed.block
