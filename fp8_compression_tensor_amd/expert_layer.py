@@ -102,6 +102,10 @@ def plain_gradients(x, weight, dy, offsets):
 
 def train(tokens: int, experts: int, width: int, steps: int, micro: int, rate: float,
           seed: int = 0) -> dict:
+    """What the command prints; ms_per_step is the mean of the steps after the first, None where
+    there is none."""
+    if steps < 1 or micro < 1:
+        raise ValueError(f"{steps} steps of {micro} micro-batches: at least one of each")
     dev = torch.device("cuda", torch.cuda.current_device())
     gen = torch.Generator(device=dev).manual_seed(seed)
     normal = lambda *s: torch.randn(*s, device=dev, generator=gen)
@@ -122,7 +126,7 @@ def train(tokens: int, experts: int, width: int, steps: int, micro: int, rate: f
         return loss.detach(), x, offsets, (2 / diff.numel() * diff.detach()).to(torch.bfloat16)
 
     losses = []
-    begun = 0.0
+    begun = None
     for step in range(steps):
         if step == 1:
             torch.cuda.synchronize()
@@ -142,7 +146,7 @@ def train(tokens: int, experts: int, width: int, steps: int, micro: int, rate: f
             weight -= rate * width * experts / micro * decompress(*main, BLOCK)
         losses.append(loss)
     torch.cuda.synchronize()
-    ms = (time.perf_counter() - begun) / max(steps - 1, 1) * 1e3
+    ms = None if begun is None else round((time.perf_counter() - begun) / (steps - 1) * 1e3, 3)
     # the gradients of one more batch against the uncompressed layer's
     _, x, offsets, dy = micro_batch(CompressedWeights(weight))
     dx, dw = plain_gradients(x.detach(), weight.detach(), dy, offsets)
@@ -153,7 +157,7 @@ def train(tokens: int, experts: int, width: int, steps: int, micro: int, rate: f
     logits = matmul(token, head, BLOCK, torch.float32)
     return {"tokens": tokens, "experts": experts, "width": width, "steps": steps,
             "loss_first": float(losses[0]), "loss_last": float(losses[-1]),
-            "dw_rel_l2": off_dw, "dx_rel_l2": off_dx, "ms_per_step": round(ms, 3),
+            "dw_rel_l2": off_dw, "dx_rel_l2": off_dx, "ms_per_step": ms,
             "logits": list(logits.shape)}
 
 

@@ -22,3 +22,11 @@ def test_second_derivatives_are_refused():
     (g,) = torch.autograd.grad(y.square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (g.square().sum() + x.square().sum()).backward()
+
+
+def test_the_time_of_a_step_is_of_steps_that_ran():
+    print("expert layer, one step and two", flush=True)
+    one = layer().train(tokens=256, experts=2, width=128, steps=1, micro=1, rate=0.4)
+    assert one["ms_per_step"] is None and one["loss_first"] == one["loss_last"]
+    two = layer().train(tokens=256, experts=2, width=128, steps=2, micro=1, rate=0.4)
+    assert 0 < two["ms_per_step"] < 10e3  # of one step, not a clock's reading
