@@ -520,6 +520,7 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
                                           f32x4 (&acc)[TM][TN]) {
   constexpr int KS = STAGES::KS, BM = STAGES::BM, CHUNK = STAGES::CHUNK;
   constexpr int NP = TM >= 8 ? 3 : TM >= 3 ? 2 : 1;  // a step's loads go out in this many shares
+  static_assert(CHUNK > 0 || NP > 1, "a step's scales are loaded with its last share");
   const int s0 = job.s0, s1 = job.s1;
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
   const int fa0 = fragment_offset(mrow, q, l16), fb0 = fragment_offset(BM + nrow, q, l16);
@@ -542,7 +543,6 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
   if constexpr (CHUNK > 0) feed.fill_scales(chunk0, p, job);
   lds_barrier();
   load(s + KS, 1, 0, NP);
-  if (NP == 1 && s + 1 < s1) feed.load_scales(s + 1);
   // where the scales of step x, in slot y, are
   const auto scales = [&](int x, int y) {
     return CHUNK > 0 ? lds.r[((x < s1 ? x : s1 - 1) >> p.shift) - chunk0] : lds.r[y];
@@ -575,7 +575,6 @@ __device__ __forceinline__ void run_steps(STAGES &lds, FEED &feed, const Product
         if (s + 1 < s1) feed.put_scales(s + 1, ahead);
         lds_barrier();
         load(s + 2 * KS, slot, 0, NP);
-        if (NP == 1 && s + 2 < s1) feed.load_scales(s + 2);
         if constexpr (CHUNK > 0) {
           const int n0 = s - team + KS, n1 = n0 + KS - 1;  // the teams' next steps
           if (n0 < s1 && (n1 >> p.shift) - chunk0 >= CHUNK) {
