@@ -972,12 +972,16 @@ using namespace tfp8;
 bool product_block_ok(int32_t block) { return block == 128 || block == 256 || block == 512; }
 
 // How long a kernel takes for tiles of bm x bn (ns): `first` and `step` a step where every compute
-// unit has one workgroup, and the same where it has all `slots` that fit.  From the times of 475 products
+// unit has one workgroup, and the same where it has `slots`, which is counted as a full round.  That many
+// are resident together, save for three float32 kernels whose registers let fewer in (64 x 64: three of
+// the four counted; with two teams, one of two; 16 x 16: three of four): there a full round is more than
+// one of the hardware's, and its time, fitted as it is, holds their sum.  From the times of 475 products
 // of each output type, of 1 to 4096 rows and 512 to 16384 columns, 640 to 5120 deep, dense, in 4
 // to 32 groups and by groups along the depth, a ninth of them with operands that no cache holds; fitted
 // so that the choice below costs least: what it picks takes 0.8% longer than the best of these
 // kernels on average for bfloat16 outputs, 1.5% for float32 (a choice by the number of rows alone took
-// 20% longer, up to 4 times as long).  slots = 0: no such kernel.
+// 20% longer, up to 4 times as long).  Products less than five steps deep lie outside the fit.
+// slots = 0: no such kernel.
 struct Pace {
   int bm, bn, threads, slots;
   int64_t first, step, first_full, step_full;

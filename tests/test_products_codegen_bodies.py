@@ -135,3 +135,37 @@ def test_planted_mistakes_are_found(kernels):
         assert m0_mistakes(code[:loads[-1] - 1] + code[loads[-1]:]), kernel  # no s_nop
         dry = [l for l in code if not re.match(r"s_waitcnt.*vmcnt\(0\)", l)]
         assert wait_mistakes(dry, "k_matmul_tile" in kernel), kernel
+
+
+def test_workgroups_a_compute_unit(kernels):
+    """kPace's slots are what registers (512 a lane of a SIMD, in eights) and LDS (160 KB) let in, save
+    for the three kernels that its comment names."""
+    name, bodies, text = kernels
+    if "matmul" not in name:
+        return
+    source = open(os.path.join(CSRC, name)).read()
+    table = re.search(r"kPace\[2\]\[kKinds\] = (.*?);", source, re.S).group(1)
+    rows = [tuple(map(int, r.split(","))) if r else None
+            for r in re.findall(r"\{([\d, ]*)\}", re.sub(r"\s+", " ", table))]
+    assert len(rows) == 14
+    slots = {(i // 7, *r[:3]): r[3] for i, r in enumerate(rows) if r}
+    fewer = {(1, 64, 64, 256): 3, (1, 64, 64, 512): 1, (1, 16, 16, 512): 3}
+    found = set()
+    for m in re.finditer(r"\.amdhsa_kernel (\S+)(.*?)\.end_amdhsa_kernel", text, re.S):
+        tile = re.search(r"k_matmul_tileILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi\d+ELi\dELb(\d)",
+                         m.group(1))
+        if tile:
+            bm, bn, wm, wn, teams, f32 = map(int, tile.groups())
+            waves = wm * wn * teams
+        else:
+            mt, tn, f32 = map(int, re.search(r"k_matmul_splitILi(\d)ELi(\d)ELi\dELb(\d)",
+                                             m.group(1)).groups())
+            bm, bn, waves = 16 * mt, 16 * tn, 8
+        of = lambda k: int(re.search(rf"\.amdhsa_{k} (\d+)", m.group(2)).group(1))
+        registers = (of("next_free_vgpr") + 7) // 8 * 8
+        fits = min(min(512 // registers, 8) * 4 // waves,
+                   160 * 1024 // of("group_segment_fixed_size"))
+        key = (f32, bm, bn, 64 * waves)
+        found.add(key)
+        assert fits == fewer.get(key, slots[key]), (key, fits)
+    assert found == set(slots)
