@@ -17,11 +17,14 @@
 // follow one another in an output row, and stores a column's four alphas and four scales as 16 bytes
 // each, where single floats would each cost a write of a line.
 //
-// Bound by HBM.  [16384, 5120] bfloat16, B = 128 (257 MB with the scales): 54 us, 4.76 TB/s, where a
-// large copy reaches 4.96; before the scales went out together and whole blocks lost their
-// per-row conditions, 67 us.  [16384, 5120] float32: 92 us, 4.6 TB/s.  Odd rows and columns: 61 us.
-// Half as many columns a lane (six wavefronts a SIMD instead of four) took 60 us; non-temporal
-// loads and stores were 1-2% faster here and 13-17% slower on data that is still in the caches.
+// Bound by HBM.  [16384, 5120] bfloat16, B = 128 (257 MB with the scales): 53 us, 4.8 TB/s, where a
+// large copy reaches 5.0 and k_compress, which reads whole rows, 42 us on the same bytes; before the
+// scales went out together and whole blocks lost their per-row conditions, 67 us.  [16384, 5120]
+// float32: 92 us, 4.6 TB/s (k_compress 66).  Odd rows and columns: 61 us.  Longer blocks take
+// more registers a lane (182 at B = 256, 227 at 512: two wavefronts a SIMD), and at 512 a load of bfloat16
+// reads half a line: 60 us at 256 and 78 at 512, float32 91 and 116.  Half as many columns a lane at
+// B = 128 (six wavefronts a SIMD instead of four) took 60 us; non-temporal loads and stores were 1-2%
+// faster here and 13-17% slower on data that is still in the caches.
 #include <math.h>
 #include <stdint.h>
 

@@ -671,22 +671,27 @@ __device__ __forceinline__ void wide_range_tile(const Job &t) {
 
 // One tile of BM x BN by WM x WN wavefronts (of KS teams).
 //
-// What bounds it.  bfloat16, tiles of 256 x 256: a matrix instruction takes 32 cycles of its unit, and
-// with the eight vector instructions of its scaled addition 48 of its SIMD.  8192 x 16384 x 4096 in
-// blocks of 256 takes 560 to 645 us on different cards, 1.7 to 1.96 PFLOP/s (a library product of
-// 8-bit operands with one scale each reaches 3.1): 4540 cycles a step, 2048 of them the matrix
-// units', at a clock that the power limit holds near 1.9 GHz.  Codes that are all zero take 13% less
-// time at the same work, and a loop over tiles that fetches the next one's codes under the stores of
-// this one gained nothing.  16384 rows in 8 groups by 5120 x 4096: 435 to 480 us, the same rate less
-// its last round of tiles, a third full.
+// What bounds it.  bfloat16, tiles of 256 x 256: 8192 x 16384 x 4096 in blocks of 256 takes 560 to
+// 645 us on different cards, 1.7 to 1.96 PFLOP/s (a library product of 8-bit operands with one scale
+// each reaches 3.1), some 4600 cycles a step, at a clock that the power limit holds near 1.9 GHz.  No one unit
+// is full: the matrix units are busy 44% of the cycles (2048 a step), half of that beside vector
+// instructions; vector instructions, eight of them with each matrix instruction for its scaled addition, take
+// 58% of a SIMD's issue and scalar ones 16%; and a wavefront waits 27% of its time for loads, LDS or the
+// barrier, and 28% for its turn to issue.  Two wavefronts a SIMD, in step at the barrier, leave gaps
+// that neither fills.  Codes that are all zero take 13% less time at the same work, and a loop over
+// tiles that fetches the next one's codes under the stores of this one gained nothing.  16384 rows in
+// 8 groups by 5120 x 4096: 435 to 480 us, the same rate less its last round of tiles, a third
+// full; the weight gradient of 16384 rows in 8 groups, 4096 x 2560 each, 230 us, 1.49 PFLOP/s.
 // float32, tiles of 128 x 128 by four wavefronts, two workgroups a compute unit: widening the codes
-// takes eight more vector instructions for each 16 x 16 tile and step, and the matrix instructions
-// have half the rate.  8192 x 8192 x 8192: 1082 us, 1.02 PFLOP/s.  8 groups of 16384 rows in all,
-// 4096 x 2560 each: 403 to 465 us, 0.74 to 0.85 PFLOP/s; a tile is 16 steps deep there.  (In tiles
-// of 256 x 128 by eight wavefronts 1093 us, and 428 where this takes 420; 6400 rows in 16 groups by
-// 5120 x 1024 152 us, against 109.)  In tiles of 64 x 64 (1003 x 2571 x 2560: 25 us) widening is
-// what bounds it: 64 of a wavefront's 104 vector instructions a step, for four 16 x 16 tiles;
-// larger tiles, which widen less, leave compute units without one.
+// takes eight more vector instructions for each 16 x 16 tile and step, each code being widened by both
+// wavefronts that use it, and the matrix instructions have half the rate.  8192 x 8192 x 8192: 1040 to
+// 1120 us, about 1.02 PFLOP/s.  8 groups of 16384 rows in all, 4096 x 2560 each: 403 to 465 us, 0.74
+// to 0.85 PFLOP/s; a tile is 16 steps deep there.  (In tiles of 256 x 128 by eight wavefronts 1093 us,
+// and 428 where this takes 420; 6400 rows in 16 groups by 5120 x 1024 152 us, against 109.)  In tiles
+// of 64 x 64 (1003 x 2571 x 2560: 25 to 28 us) widening is 64 of a wavefront's 104 vector instructions
+// a step, for four 16 x 16 tiles, again twice for each code; they fill somewhat over half of the issue
+// while a compute unit has a workgroup, which, with 2.6 tiles for each, is some 70% of the time.
+// Larger tiles, which widen less, leave compute units without one.
 //
 // The kernel only calls this function: a kernel's own body is also read by the host's pass, which
 // does not know these builtins.
@@ -781,10 +786,12 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_matmul_tile(ProductArg
 // instruction in the order of the lanes, come at 9.6 TB/s over the chip, from the L1 cache too; whole
 // lines through LDS come at 28.)
 //
-// 24 x 10240 x 5120: 13.9 us, 4.1 TB/s, in 32 x 48 tiles (14.5 in 32 x 64, 19 in 32 x 32, whose 320
-// workgroups are more than one round); 48 rows in 16 groups, 2560 x 4096 each: 36 us, 4.7 TB/s, where a
-// large copy reaches 5.0.  One row of 4096 x 4096, 2.9 TB/s, takes 6.2 us, of which its bytes are 3.6
-// and the start, the first loads' latency and the sum over the wavefronts the rest.  Scales are prepared in LDS, kSplitBlocks blocks at a time.
+// 24 x 10240 x 5120: 14.1 us, 4.0 TB/s, in 32 x 48 tiles (14.5 in 32 x 64, 19 in 32 x 32, whose 320
+// workgroups are more than one round); 48 rows in 16 groups, 2560 x 4096 each: 36 us, 4.7 TB/s.  (The
+// compress kernel streams 6.1 TB/s from HBM; of three operands read in turn here a part stays in the 256 MB
+// cache.)  One row of 4096 x 4096, 2.9 TB/s, takes 6.2 us, of which its bytes are 2.9 and the start,
+// the first loads' latency and the sum over the wavefronts the rest.  Scales are prepared in LDS,
+// kSplitBlocks blocks at a time.
 constexpr int kSplitWaves = 8, kSplitBlocks = 64;
 
 // 32 codes of a lane, as stored.
