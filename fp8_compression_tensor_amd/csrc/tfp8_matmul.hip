@@ -310,8 +310,10 @@ __device__ __forceinline__ bool find_job(const ProductArgs &p, Job &t) {
 // block's sum.  An r below float32's normal range (blocks of values below about 2^-115) has lost
 // bits, which is below 2^-123 of a result for each kStep codes as long as the other operand's r is
 // at most 1.  A tile where an r of one operand may be so small (alpha above 2^84: every r below 2^-126
-// has one, whatever its target) and one of the other above 1 is computed again by wide_range_tile.
-enum : int { kTinyA = 1, kLargeA = 2, kTinyB = 4, kLargeB = 8 };
+// has one, whatever its target) and one of the other above 1 is computed again by wide_range_tile; so
+// is one where both have an r above 2^31 (no r reaches 2^96), whose product may be infinite and make NaN
+// of a sum that is 0.
+enum : int { kTinyA = 1, kLargeA = 2, kHugeA = 4, kTinyB = 8, kLargeB = 16, kHugeB = 32 };
 
 // Notes four blocks of a row of each lane, the rows all of A or all of B; as integers, which order like
 // these positive floats.  Noting and asking at the end take 1% of a large product, 0.2 us of one of
@@ -323,10 +325,14 @@ __device__ __forceinline__ void note_range(const f32x4 s, const f32x4 alpha, boo
     a[i] = __float_as_int(alpha[i]);
     most = max(most, __float_as_int(s[i]));
   }
+  const int least = min(min(a[0], a[1]), min(a[2], a[3]));
   const uint64_t tiny = __ballot(max(max(a[0], a[1]), max(a[2], a[3])) > __float_as_int(0x1p84f));
-  const uint64_t large = __ballot(most > min(min(a[0], a[1]), min(a[2], a[3])));
-  if (__builtin_expect((tiny | large) != 0, 0))
-    saw |= (tiny ? (is_a ? kTinyA : kTinyB) : 0) | (large ? (is_a ? kLargeA : kLargeB) : 0);
+  const uint64_t large = __ballot(most > least);
+  if (__builtin_expect((tiny | large) != 0, 0)) {
+    const uint64_t huge = __ballot(__int_as_float(most) > 0x1p31f * __int_as_float(least));
+    const int seen = (tiny ? kTinyA : 0) | (large ? kLargeA : 0) | (huge ? kHugeA : 0);
+    saw |= is_a ? seen : seen * (kTinyB / kTinyA);
+  }
 }
 
 // A wavefront's `saw` to its word of LDS, and, after a barrier, a wavefront's word to each lane and
@@ -339,7 +345,8 @@ __device__ __forceinline__ int told(const float *words) {
 __device__ __forceinline__ bool wide_range(int word) {
   if (__builtin_expect(__ballot(word) == 0, 1)) return false;
   return (__ballot(word & kTinyA) && __ballot(word & kLargeB)) ||
-         (__ballot(word & kTinyB) && __ballot(word & kLargeA));
+         (__ballot(word & kTinyB) && __ballot(word & kLargeA)) ||
+         (__ballot(word & kHugeA) && __ballot(word & kHugeB));
 }
 
 // LDS of a tile: two stages of a step's codes, A's rows then B's (four measured no

@@ -176,14 +176,14 @@ tfp8_status tfp8_accumulate(const uint8_t *codes, const float *alpha, const floa
  *   C[m][n] = sum over blocks (s_a / alpha_a)(s_b / alpha_b) sum_k dec(qa[m][k]) dec(qb[n][k]),
  * the sum over blocks in float32.  The factors s / alpha are float32 as well, save in tiles of the
  * output where one operand's may lie below its normal range (alpha above 2^84) and one of the other's
- * above 1: there they, and the sum over blocks, are float64, and the tile takes several times as
- * long.  Beside the roundings of its sum a result is thus off by less than 2^-123 for each 128 of k.
+ * above 1, or where both operands have one above 2^31: there they, and the sum over blocks, are
+ * float64, and the tile takes several times as long.  Beside the roundings of its sum a result is thus off by less than 2^-123 for each 128 of k.
  * A block's sum is float32 throughout for float32 outputs.  For bfloat16 outputs it is the 8-bit
  * matrix instructions', which add eight products of neighbouring codes at a time with 14 bits from
  * the largest one's down, and the eights in float32: about 1.4e-5 of the result, a hundredth of the
  * output's own rounding, at twice the rate.  E4M3 codes only, made by the calls above (the codes of
  * NaN, 0x7F and 0xFF, do not occur and are outside the contract).  A partial sum above float32's
- * range gives an infinity or NaN, as it would with the uncompressed operands.
+ * range may give an infinity or NaN.
  *
  * Common rules: block is 128, 256 or 512 (TFP8_E_BLOCK); rows at most 2^31 - 1, k a multiple of
  * block and at most 2^22 (TFP8_E_SIZE); ld >= k and lds >= k / block (TFP8_E_ARG), ld at most 2^22

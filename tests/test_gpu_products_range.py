@@ -102,3 +102,17 @@ def test_subnormal_gradients_by_ordinary_values(m, n, k, dt):
     # as a part of the magnitudes that the bound counts at 2^-16 and more of them
     mag = mag + k // 128 * 2.0 ** (16 - 123)
     assert_product(got, (e, mag, mag2), k, f"{m}x{n}x{k}")
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(5, 100, 256), (90, 9000, 1152), (300, 300, 640), (1537, 2561, 640)])
+def test_huge_values_that_do_not_meet(m, n, k, dt):
+    """Without the rotation, one value of 2^80 to 2^99 a block, at other places in a than in b: the
+    product of the factors leaves float32's range, and the sums are 0."""
+    say(f"matmul {m}x{n}x{k} {dt}, huge values at different places")
+    block, off = 128, tfp8.FLAG_NO_ROTATION
+    a, b = torch.zeros(m, k, device=DEV), torch.zeros(n, k, device=DEV)
+    a[:, 3::block] = torch.exp2(80 + torch.arange(m, device=DEV) % 20).float()[:, None]
+    b[:, 70::block] = -torch.exp2(99 - torch.arange(n, device=DEV) % 20).float()[:, None]
+    a, b = tfp8.compress(a, block, flags=off), tfp8.compress(b, block, flags=off)
+    assert not tfp8.matmul(a, b, block, DTYPES[dt]).any()
