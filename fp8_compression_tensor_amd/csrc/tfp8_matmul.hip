@@ -683,11 +683,11 @@ __device__ __forceinline__ void wide_range_tile(const Job &t) {
 // each reaches 3.1), some 4600 cycles a step, at a clock that the power limit holds near 1.9 GHz.  No one unit
 // is full: the matrix units are busy 44% of the cycles (2048 a step), half of that beside vector
 // instructions; vector instructions, eight of them with each matrix instruction for its scaled addition, take
-// 58% of a SIMD's issue and scalar ones 16%; and a wavefront waits 27% of its time for loads, LDS or the
+// 59% of a SIMD's issue and scalar ones 16%; and a wavefront waits 26% of its time for loads, LDS or the
 // barrier, and 28% for its turn to issue.  Two wavefronts a SIMD, in step at the barrier, leave gaps
 // that neither fills.  Codes that are all zero take 13% less time at the same work, and a loop over
 // tiles that fetches the next one's codes under the stores of this one gained nothing.  16384 rows in
-// 8 groups by 5120 x 4096: 435 to 480 us, the same rate less its last round of tiles, a third
+// 8 groups by 5120 x 4096: 435 to 484 us, the same rate less its last round of tiles, a third
 // full; the weight gradient of 16384 rows in 8 groups, 4096 x 2560 each, 230 us, 1.49 PFLOP/s.
 // float32, tiles of 128 x 128 by four wavefronts, two workgroups a compute unit: widening the codes
 // takes eight more vector instructions for each 16 x 16 tile and step, each code being widened by both
@@ -695,7 +695,7 @@ __device__ __forceinline__ void wide_range_tile(const Job &t) {
 // 1120 us, about 1.02 PFLOP/s.  8 groups of 16384 rows in all, 4096 x 2560 each: 403 to 465 us, 0.74
 // to 0.85 PFLOP/s; a tile is 16 steps deep there.  (In tiles of 256 x 128 by eight wavefronts 1093 us,
 // and 428 where this takes 420; 6400 rows in 16 groups by 5120 x 1024 152 us, against 109.)  In tiles
-// of 64 x 64 (1003 x 2571 x 2560: 25 to 28 us) widening is 64 of a wavefront's 104 vector instructions
+// of 64 x 64 (1003 x 2571 x 2560: 25 to 29 us) widening is 64 of a wavefront's 104 vector instructions
 // a step, for four 16 x 16 tiles, again twice for each code; they fill somewhat over half of the issue
 // while a compute unit has a workgroup, which, with 2.6 tiles for each, is some 70% of the time.
 // Larger tiles, which widen less, leave compute units without one.
