@@ -323,6 +323,12 @@ __device__ __forceinline__ uint32_t bf16_nearest(float x) {
   return __builtin_bit_cast(uint16_t, (__bf16)x);
 }
 
+// The square root by hardware, which takes a subnormal value for 0: such a one is scaled first, by a power of 4.
+__device__ __forceinline__ float root_of(float v) {
+  const bool small = v < 0x1p-126f;
+  return __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v) * (small ? 0x1p-32f : 1.0f);
+}
+
 // Four neighbouring elements, as they lie in memory, where `rem` of them are there.
 template <bool WHOLE>
 __device__ __forceinline__ u32x4 load4_f32(const float *p, int rem) {
@@ -652,7 +658,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(StepTable<(GT == kGradCodes 
       v[i] *= old_v[q / QB];
       if constexpr (BITS == 8) v[i] *= v[i];
       v[i] = fmaf(gv, gv, v[i]);
-      const float r = __builtin_amdgcn_sqrtf(v[i]);
+      const float r = root_of(v[i]);
       const float u = m[i] * __builtin_amdgcn_rcpf(fmaf(r, f.root, a.eps));
       x[i] = fmaf(-f.rate, u, p[i] * f.keep);
       m1[4 * q + i] = m[i];

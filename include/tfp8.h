@@ -303,6 +303,8 @@ typedef struct {
  *   p' = (1 - lr wd) p - lr / (1 - beta1^t) * m' / (sqrt(v') / sqrt(1 - beta2^t) + eps).
  * Arithmetic is float32; the factors of a step are float64, rounded once.  A grad_scale that is infinite or
  * NaN leaves the step out: params and copies stay as they were, and the new states are the old ones.
+ * States of 32 bits hold v' itself: where sqrt(1 - beta2) |g| is below 2^-63 it has fewer bits, below 2^-75
+ * none, so that an eps below about 2^-70 does not hold such a step back.
  *
  * States are flat, and go from m, v to m_out, v_out: each of these four and their scales is exactly
  * its input (in place) or apart from all else.  Element i of a tensor has its states at start + i, start a multiple of block, the
