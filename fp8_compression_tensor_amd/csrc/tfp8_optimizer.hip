@@ -656,9 +656,15 @@ __global__ __launch_bounds__(kThreads) void k_adamw(StepTable<(GT == kGradCodes 
       const float gv = g[4 * q + i] * to_v;
       m[i] = fmaf(g[4 * q + i], to_m, m[i] * old_m[q / QB]);
       v[i] *= old_v[q / QB];
-      if constexpr (BITS == 8) v[i] *= v[i];
-      v[i] = fmaf(gv, gv, v[i]);
-      const float r = root_of(v[i]);
+      float r;
+      if constexpr (BITS == 8) {  // scaled: the squares may leave float32's range where the root does not
+        const int k = exponent_of(fmaxf(fabsf(v[i]), fabsf(gv)));
+        const float old = scale2(v[i], -k), now = scale2(gv, -k);
+        r = scale2(__builtin_amdgcn_sqrtf(fmaf(now, now, old * old)), k);
+      } else {
+        v[i] = fmaf(gv, gv, v[i]);
+        r = root_of(v[i]);
+      }
       const float u = m[i] * __builtin_amdgcn_rcpf(fmaf(r, f.root, a.eps));
       x[i] = fmaf(-f.rate, u, p[i] * f.keep);
       m1[4 * q + i] = m[i];
@@ -709,7 +715,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(StepTable<(GT == kGradCodes 
       mm = lanes_max<G>(fabsf(mm));
       rm = lanes_max<G>(fabsf(rm));
       const float im = mm < 0x1p-100f ? 0.0f : 448.0f * __builtin_amdgcn_rcpf(mm);
-      const float ir = rm == 0.0f ? 0.0f : 448.0f * __builtin_amdgcn_rcpf(rm);
+      const float ir = rm < 0x1p-100f ? 0.0f : 448.0f * __builtin_amdgcn_rcpf(rm);
 #pragma unroll
       for (int q = QB * k; q < QB * (k + 1); ++q) {
         const int o = off(q, at_p, bw), oi = off(q, at_p, bw_in), left4 = rem(o);
@@ -719,7 +725,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(StepTable<(GT == kGradCodes 
         for (int i = 0; i < 4; ++i) {
           h[i] = random(oi, i);
           m[i] = __builtin_amdgcn_fmed3f(m1[4 * q + i] * im, -448.0f, 448.0f);
-          r[i] = r1[4 * q + i] > 0.0f
+          r[i] = r1[4 * q + i] > 0.0f && !(rm < 0x1p-100f)
                      ? __builtin_amdgcn_fmed3f(r1[4 * q + i] * ir, kSmallestCode, 448.0f) : 0.0f;
         }
         const uint32_t dm = codes_of(m, [&](int i) { return h[i] << 16 | 0x8000u; });
@@ -745,7 +751,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(StepTable<(GT == kGradCodes 
                              : lane % G == 0 && 256 * QB * k + 4 * lane < left;
       if (first) {
         a.m_scale_out[state0 / B + block_of(k)] = mm < 0x1p-100f ? 0.0f : mm * (1.0f / 448.0f);
-        a.v_scale_out[state0 / B + block_of(k)] = rm * (1.0f / 448.0f);
+        a.v_scale_out[state0 / B + block_of(k)] = rm < 0x1p-100f ? 0.0f : rm * (1.0f / 448.0f);
       }
     }
   }

@@ -314,8 +314,8 @@ typedef struct {
  * of the second moment, sqrt(v) = v_scale * dec(v); all zeros to begin with.  A scale is the block's
  * largest magnitude / 448.  Codes are rounded stochastically, up with the probability of the part
  * that is cut off, because a step moves a second moment by less than half a code; a root other than 0
- * is rounded to no less than the smallest code, because it divides.  A block whose first moments are
- * all below 2^-100 is stored as zeros.  bfloat16 params are rounded stochastically too (copies to
+ * is rounded to no less than the smallest code, because it divides.  A block whose first moments, or
+ * whose roots, are all below 2^-100 is stored as zeros.  bfloat16 params are rounded stochastically too (copies to
  * nearest even).  The random bits of element i of the states are a hash of seed, t and i: the same
  * arguments give the same result.
  *
