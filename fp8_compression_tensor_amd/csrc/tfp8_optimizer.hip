@@ -1049,8 +1049,9 @@ tfp8_status adamw(const tfp8_adamw_tensor *tensors, int32_t count, int32_t block
     if (x.start < 0 || x.start > TFP8_MAX_N || x.start % block != 0 || (codes && n % block != 0))
       return TFP8_E_SIZE;
     if (n == 0) continue;
-    if (x.start < end || x.start + n > state_n) return TFP8_E_ARG;
+    if (x.start < end) return TFP8_E_ARG;
     end = (x.start + n + block - 1) / block * block;
+    if (end > state_n) return TFP8_E_ARG;  // its last block has a scale, too
     if (!x.param || (x.copy_dtype != TFP8_NONE && !x.copy) ||
         (codes && (!x.copy_alpha || !x.copy_scale)))
       return TFP8_E_NULL;
@@ -1073,7 +1074,7 @@ tfp8_status adamw(const tfp8_adamw_tensor *tensors, int32_t count, int32_t block
   }
   if (!any) return TFP8_OK;
   // each of the four states: where it comes from, where it goes to, its bytes and alignment
-  const int64_t each = bits == 8 ? state_n : state_n * 4, scales = (state_n + block - 1) / block * 4;
+  const int64_t each = bits == 8 ? state_n : state_n * 4, scales = state_n / block * 4;
   const struct {
     const void *in, *out;
     int64_t bytes;

@@ -225,3 +225,22 @@ def test_step_rows_arguments():
     for bad in (bytes(8), None):
         with pytest.raises((BufferError, TypeError)):
             optimizer._address(bad)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_states_hold_whole_blocks(bits):
+    """A tensor's part of the states is rounded up to whole blocks, of which states of 8 bits have a scale each:
+    with 1000 elements in states of 1000, the scale of the eighth block would lie past the seven."""
+    odd = (STATE[0] + 2, *STATE[1:])  # refused after the tensors: no call here gets past the checks
+    for n in (1000, 1023):
+        assert step([DENSE], bits=bits, state=odd, n=n) == -6
+        assert step([put(DENSE, START=1024)], bits=bits, state=odd, n=1024 + n) == -6
+    assert step([put(DENSE, N=1)], block=512, bits=bits, state=odd, n=511) == -6
+    assert step([DENSE], bits=bits, state=odd, n=1024) == -5
+    assert step([put(DENSE, N=896)], bits=bits, state=odd, n=1000) == -5
+
+
+def test_scales_of_whole_blocks():
+    """States of 1000 have seven scales: the two lists of them may not share the seventh."""
+    shared = (STATE[0], STATE[1], STATE[2], STATE[1] + 24)
+    assert step([put(DENSE, N=896)], state=shared, n=1000) == -6
