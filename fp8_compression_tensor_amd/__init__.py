@@ -36,6 +36,7 @@ SUPPORTED_BLOCKS = (64, 128, 256, 512)
 PRODUCT_BLOCKS = (128, 256, 512)  # blocks that the products of compressed operands take
 MAX_GROUPS = 65536
 MOE_TOKENS, MOE_EXPERTS = 64, 512  # the most that moe_layer takes
+_MOE_ALL_EXPERTS = 4  # TFP8_MOE_ALL_EXPERTS (include/tfp8.h)
 
 _STATUS = {0: "TFP8_OK", -1: "TFP8_E_NULL", -2: "TFP8_E_SIZE", -3: "TFP8_E_BLOCK",
            -4: "TFP8_E_DTYPE", -5: "TFP8_E_ALIGN", -6: "TFP8_E_ARG", -7: "TFP8_E_HIP"}
@@ -658,6 +659,8 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, up, down, top_k: int, block
     products run on compressed activations."""
     _product_block(block)
     dt = _out_dtype(dtype)
+    if flags & ~FLAG_NO_ROTATION:
+        _check(-6)  # TFP8_E_ARG, as the C call gives it for the flags that it does not know
     for t, name in ((x, "x"), (router, "router")):
         if not (isinstance(t, torch.Tensor) and t.is_cuda):
             raise ValueError("tfp8 operates on GPU tensors only (no CPU path)")
@@ -692,7 +695,7 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, up, down, top_k: int, block
     raw = lambda t: (t.data_ptr(), BF16 if t.dtype == torch.bfloat16 else F32)
     _run(x, moe_layer_raw, (*raw(x), x.stride(0) if tokens > 1 else k), raw(router),
          (ru[0], ru[2], ru[3]), (rd[0], rd[2], rd[3]), tokens, experts, top_k, k, f, block,
-         flags | (0 if renormalize else 4), workspace.data_ptr(), nbytes,
+         flags | (0 if renormalize else _MOE_ALL_EXPERTS), workspace.data_ptr(), nbytes,
          (out.data_ptr(), dt, ldo), _stream(x))
     if given:  # a graph that has saved it is not to be run backward through its new values
         torch.autograd.graph.increment_version(out)

@@ -56,3 +56,15 @@ def test_most_hidden_values():
     assert call(tokens=64, experts=512, top_k=512, f=1 << 14, nbytes=1 << 40) == -2
     assert tfp8.lib().tfp8_moe_workspace(64, 512, 512, 256, 1 << 14) == 0
     assert tfp8.lib().tfp8_moe_workspace(64, 512, 512, 256, (1 << 14) - 128) > 0
+
+
+def test_flags_of_the_wrapper():
+    """Only FLAG_NO_ROTATION: the C call's bit for the softmax of all is renormalize's."""
+    import torch
+
+    x = torch.zeros(1, 128)
+    for flags in (4, 4 | tfp8.FLAG_NO_ROTATION, tfp8.FLAG_INT8, 8, -1):
+        with pytest.raises(tfp8.TFP8Error, match="TFP8_E_ARG"):
+            tfp8.moe_layer(x, x, (), (), 1, flags=flags)
+    with pytest.raises(ValueError, match="GPU"):
+        tfp8.moe_layer(x, x, (), (), 1, flags=tfp8.FLAG_NO_ROTATION)
