@@ -175,8 +175,9 @@ class GatedExperts:
 
     def __init__(self, router, up, down, top_k: int, block: int = BLOCK, bits: int = 8, seed: int = 0):
         self.params = [p.detach().clone().requires_grad_() for p in (router, up, down)]
-        self.top_k, self.block, self.seed, self.steps = top_k, block, seed, 0
+        self.top_k, self.block, self.seed = top_k, block, seed
         self.state = adamw_state(self.params, bits, block)
+        self.steps = torch.zeros((), dtype=torch.int64, device=self.params[0].device)  # that were taken
         self.rows = [compress(p.detach(), block) for p in self.params[1:]]
         self._lay_out()
 
@@ -204,12 +205,14 @@ class GatedExperts:
 
     def step(self, grads, rate: float, max_norm: float = 1.0, decay: float = 0.0) -> torch.Tensor:
         """One AdamW step from the parameters' gradients, dense or compressed, clipped together; returns
-        their norm.  The step writes the weights' new codes."""
-        self.steps += 1
+        their norm.  The step writes the weights' new codes.  Where the norm is infinite or NaN it is left out,
+        and does not count: the number of steps lies on the GPU, which alone knows."""
         norm, scale = grad_norm(grads, max_norm, self.block)
+        steps = self.steps + torch.isfinite(scale)
         adamw([p.detach() for p in self.params], grads, self.state, rate, (0.9, 0.99),
-              weight_decay=decay, step=self.steps, block=self.block, scale=scale,
+              weight_decay=decay, step=steps, block=self.block, scale=scale,
               copies=[None, *self.rows], seed=self.seed)
+        self.steps = steps
         self._lay_out()
         return norm
 
