@@ -200,7 +200,7 @@ class GatedExperts:
         h = (torch.nn.functional.silu(a[:, :f].float()) * a[:, f:].float()).to(x.dtype)
         y = expert_linear(h, down, self.compressed[1], offsets)
         back = torch.empty_like(order).scatter_(0, order, torch.arange(len(order), device=x.device))
-        y = y[back].view(len(x), self.top_k, -1).float()
+        y = y[back].view(len(x), self.top_k, y.shape[-1]).float()
         return (y * gates[..., None]).sum(1).to(x.dtype)
 
     def step(self, grads, rate: float, max_norm: float = 1.0, decay: float = 0.0) -> torch.Tensor:

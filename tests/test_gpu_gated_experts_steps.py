@@ -26,3 +26,19 @@ def test_a_step_that_is_left_out_does_not_count(bits, bad):
             assert torch.equal(a, b), i
         for a, b in zip([*L.state, *L.rows[0], *L.rows[1]], [*twin.state, *twin.rows[0], *twin.rows[1]]):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("top_k", [1, 3])
+def test_no_tokens(top_k):
+    """Outputs and gradients of no tokens at all."""
+    print("gated experts, no tokens", top_k, flush=True)
+    L, gen = layer(top_k=top_k)
+    x = torch.randn(0, 256, device=DEV, generator=gen).to(torch.bfloat16).requires_grad_()
+    y = L(x)
+    assert y.shape == (0, 256) and y.dtype == x.dtype
+    y.float().sum().backward()
+    assert x.grad.shape == (0, 256)
+    for p in L.params:
+        assert p.grad is not None and not p.grad.any()
+    with torch.no_grad():
+        assert L.answer(x).shape == (0, 256)
