@@ -174,6 +174,8 @@ class GatedExperts:
     largest logits, weighted by their softmax."""
 
     def __init__(self, router, up, down, top_k: int, block: int = BLOCK, bits: int = 8, seed: int = 0):
+        if not 1 <= top_k <= len(router):
+            raise ValueError(f"top_k must be 1 to {len(router)}, got {top_k}")
         self.params = [p.detach().clone().requires_grad_() for p in (router, up, down)]
         self.top_k, self.block, self.seed = top_k, block, seed
         self.state = adamw_state(self.params, bits, block)
