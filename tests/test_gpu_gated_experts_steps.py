@@ -1,8 +1,10 @@
-"""GatedExperts' steps: which of them count."""
+"""GatedExperts' steps: which of them count, and what they do to the parameters."""
 import pytest
 import torch
 
+import fp8_compression_tensor_amd as tfp8
 from test_gpu_gated_experts import layer
+from test_gpu_optimizer import check_step
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -42,3 +44,39 @@ def test_no_tokens(top_k):
         assert p.grad is not None and not p.grad.any()
     with torch.no_grad():
         assert L.answer(x).shape == (0, 256)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_steps_are_adamws(bits):
+    """Parameters, states and codes after the steps of a layer that follows another one: AdamW's, in float64,
+    from the gradients of two micro-batches, the experts' added up in codes, and clipped."""
+    print("gated experts, steps against the formula", bits, flush=True)
+    (L, gen), (teacher, _) = layer(bits=bits), layer(seed=1)
+    clipped = 0
+    for step in (1, 2, 3):
+        main = None
+        for _ in range(2):
+            x = torch.randn(200, 256, device=DEV, generator=gen).to(torch.bfloat16)
+            with torch.no_grad():
+                want = teacher(x)
+            (L(x) - want).float().square().mean().backward()
+            grads = [p.grad for p in L.params]
+            for p in L.params:
+                p.grad = None
+            if main is None:
+                main = [grads[0], *(tfp8.compress(g) for g in grads[1:])]
+            else:
+                main[0] += grads[0]
+                for m, g in zip(main[1:], grads[1:]):
+                    tfp8.accumulate(*m, g, inplace=True)
+        before = [p.detach().flatten().clone() for p in L.params]
+        old = tuple(t.clone() for t in L.state)
+        most = 0.05 if step < 3 else 1e3
+        c = float(tfp8.grad_norm(main, most)[1])
+        clipped += c < 1
+        L.step(main, 2e-3, most, 0.1)
+        flat = [main[0].flatten(), *main[1:]]
+        codes = [None, *((c.flatten(), a.flatten(), s.flatten()) for c, a, s in L.rows)]
+        check_step([p.detach().flatten() for p in L.params], before, flat, old, L.state, codes, 128, step,
+                   c=c, lr=2e-3)
+    assert clipped == 2 and int(L.steps) == 3
