@@ -286,27 +286,31 @@ __global__ __launch_bounds__(EXPERTS >= 256 ? 1024 : 256) void k_moe_plan(MoeArg
   }
 }
 
-// The same choice by a workgroup of four wavefronts for itself, for up to 4 tokens and 64 experts.  Lane e
-// of wavefront w compares expert e of token w % tokens with a part of the others.
+// Up to this many tokens k_moe_up chooses and k_moe_down rotates (one token, 8 of 64 experts of 2048 x
+// 1024: 23.3 us a call, with launches of their own 26.8; 2 tokens 37.5 and 39.0; 4 tokens, 4 of 16 of
+// 1280 x 640: 35.5 and 33.9).
+constexpr int kAlone = 2;
+
+// The same choice by a workgroup of four wavefronts for itself, for one or two tokens and up to 64 experts.
+// Lane e of wavefront w compares expert e of token w % tokens with a quarter or a half of the others.
 struct Choice {
-  double l[4][64];
-  int ranks[4][64], where[4][64], ids[4 * 64];
+  double l[kAlone][64];
+  int ranks[4][64], where[kAlone][64], ids[kAlone * 64];
 };
+static_assert(kAlone == 2, "the wavefronts share the tokens evenly, and a lane's token is its last bit");
 __device__ __forceinline__ void choose(const MoeArgs &a, Choice &c, bool tell) {
   const int lane = threadIdx.x & 63, E = a.experts;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int parts = 4 / a.tokens, t = w % a.tokens, part = w / a.tokens;  // 3 tokens: one part
+  const int parts = 4 / a.tokens, t = w % a.tokens, part = w / a.tokens;
   const double logit = lane < E ? a.logits[t * E + lane] : -__builtin_inf();
   const double mine = logit != logit ? __builtin_inf() : logit;
   c.l[t][lane] = mine;  // by each part's wavefront, the same
   __syncthreads();
   int rank = 0;
-  if (part < parts) {
-    const int from = part * (64 / parts);
+  const int from = part * (64 / parts);
 #pragma unroll 8
-    for (int o = from; o < from + 64 / parts; ++o)
-      rank += c.l[t][o] > mine || (c.l[t][o] == mine && o < lane);
-  }
+  for (int o = from; o < from + 64 / parts; ++o)
+    rank += c.l[t][o] > mine || (c.l[t][o] == mine && o < lane);
   c.ranks[w][lane] = rank;
   __syncthreads();
   if (part == 0) {
@@ -553,7 +557,7 @@ __device__ __forceinline__ Slot slot_of(const MoeArgs &a, const Choice &c, int s
   const bool by_pair = a.tokens * a.top_k < a.experts;
   Slot s;
   s.expert = by_pair ? __builtin_amdgcn_readfirstlane(c.ids[slot]) : slot;
-  s.pair = lane < a.tokens ? c.where[lane & 3][s.expert] : -1;
+  s.pair = lane < a.tokens ? c.where[lane & 1][s.expert] : -1;
   s.set = __ballot(s.pair >= 0);
   if (by_pair && s.set && __builtin_ctzll(s.set) != slot / a.top_k) s.set = 0;
   return s;
@@ -786,11 +790,6 @@ namespace {
 constexpr int kMostK = 1 << 20;  // of k and f
 constexpr int64_t kMostHidden = (int64_t)1 << 29;  // of all pairs: k_moe_up has 8 threads each, below 2^32
 
-// Up to this many tokens k_moe_up chooses and k_moe_down rotates (one token, 8 of 64 experts of 2048 x
-// 1024: 23.3 us a call, with launches of their own 26.8; 2 tokens 37.5 and 39.0; 4 tokens, 4 of 16 of
-// 1280 x 640: 35.5 and 33.9).
-constexpr int kAlone = 2;
-
 // Rows of an output tile of k_moe_down, and how many workgroups share its experts.
 // 8 rows where that fills the compute units (one token, 8 of 64 experts of 2048 x 1024: 24.1 us a call
 // against 25.1), unless the wavefronts have many slots each, which then take as long to look up as to read
@@ -871,18 +870,18 @@ tfp8_status launch_layer(const MoeArgs &a, hipStream_t st) {
   tfp8_status s = launch(k_moe_scores<B>, (unsigned)(a.tokens + a.experts * groups), kScoreThreads, st,
                          a);
   if (s != TFP8_OK) return s;
-  // k_moe_up chooses, unless it has many workgroups, each of which would (2 tokens, 2 of 8 experts of
-  // 4096 x 14336, 3584 workgroups: 102 us against 86)
-  const bool choose = a.tokens <= kAlone && a.experts <= 64 && slots * (a.f / 16) <= 1024;
+  const int64_t ups = slots * (a.f / (16 * kUpTiles));  // workgroups of k_moe_up
+  // it chooses, unless these are many, each of which would (2 tokens, 2 of 8 experts of 4096 x 14336, 1792
+  // workgroups: 102 us against 86)
+  const bool choose = a.tokens <= kAlone && a.experts <= 64 && ups <= 512;
   if (!choose) {
     s = a.experts <= 64    ? launch(k_moe_plan<64>, a.tokens, 256, st, a)
         : a.experts <= 256 ? launch(k_moe_plan<256>, a.tokens, 1024, st, a)
                            : launch(k_moe_plan<512>, a.tokens, 1024, st, a);
     if (s != TFP8_OK) return s;
   }
-  const unsigned ups = (unsigned)(slots * (a.f / (16 * kUpTiles)));
-  s = choose ? launch(k_moe_up<LO, true>, ups, 64 * kUpWaves, st, a)
-             : launch(k_moe_up<LO, false>, ups, 64 * kUpWaves, st, a);
+  s = choose ? launch(k_moe_up<LO, true>, (unsigned)ups, 64 * kUpWaves, st, a)
+             : launch(k_moe_up<LO, false>, (unsigned)ups, 64 * kUpWaves, st, a);
   if (s != TFP8_OK) return s;
   const int rows = down_rows(a.tokens, pairs, a.k);
   const bool near = a.tokens <= kAlone && a.splits == 1 && pairs * a.f <= kNear;  // k_moe_down rotates

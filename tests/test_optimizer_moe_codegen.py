@@ -73,3 +73,21 @@ def test_the_products_read_codes_through_wide_loads(kernels):
             # two wavefronts a SIMD at least: 256 registers each
             found = re.search(rf"\.amdhsa_kernel {kernel}\b.*?\.amdhsa_next_free_vgpr (\d+)", text, re.S)
             assert int(found.group(1)) <= 256
+
+
+def test_the_choice_in_the_products_holds_what_its_tokens_need(kernels):
+    """k_moe_up's own choice, for two tokens at most: logits, ranks of four wavefronts, places and experts of 64
+    experts each, beside the sums of four wavefronts."""
+    name, bodies, text = kernels
+    if "moe" not in name:
+        return
+    sums = 4 * 2 * 4 * 64 * 4
+    choice = 2 * 64 * 8 + 4 * 64 * 4 + 2 * 64 * 4 + 2 * 64 * 4
+    seen = set()
+    for kernel in bodies:
+        if "k_moe_up" in kernel:
+            found = re.search(rf"\.amdhsa_kernel {kernel}\b.*?\.amdhsa_group_segment_fixed_size (\d+)", text, re.S)
+            chooses = "Lb1EEEv" in kernel  # the last template argument
+            seen.add(chooses)
+            assert int(found.group(1)) == sums + (choice if chooses else 0), kernel
+    assert seen == {True, False}
