@@ -66,13 +66,19 @@ def build(verbose: bool = False, extra: list[str] | None = None, out: str | None
     with tempfile.TemporaryDirectory() as d:
         objects = [os.path.join(d, os.path.basename(s) + ".o") for s in SOURCES]
         jobs = [["hipcc", *flags, "-c", "-o", o, s] for s, o in zip(SOURCES, objects)]
-        if with_rows:
-            jobs.append(rows_command(ROWS + ".tmp"))
-        with ThreadPoolExecutor(len(jobs)) as pool:
+        with ThreadPoolExecutor(len(jobs) + 1) as pool:
+            rows = pool.submit(lambda: run(rows_command(ROWS + ".tmp"))) if with_rows else None
             list(pool.map(run, jobs))
         run(["hipcc", "--offload-arch=gfx950", "-shared", "-o", tmp, *objects])
     os.replace(tmp, out)
     if with_rows:
+        try:
+            rows.result()
+        except Exception as e:  # no g++, no headers of Python or torch: the rest works without
+            if os.path.exists(ROWS):  # an older library's
+                os.remove(ROWS)
+            raise RuntimeError(f"{out} is built, the module _rows.so is not, which grad_norm and adamw need: "
+                               f"{e}") from e
         os.replace(ROWS + ".tmp", ROWS)
     return out
 
