@@ -10,11 +10,15 @@ from __future__ import annotations
 import ctypes
 import math
 
-import numpy as np
 import torch
 
 from . import (BF16, F32, SUPPORTED_BLOCKS, _need_buf, _run, _stream, adamw_raw,
                grad_norm_raw, lib)
+
+try:
+    import numpy as np
+except ImportError:  # the rest of the package works without
+    np = None
 
 CODES, NONE = 2, -1  # TFP8_CODES and TFP8_NONE (include/tfp8.h)
 _DENSE = {torch.bfloat16: BF16, torch.float32: F32}
@@ -68,6 +72,13 @@ def _load():
                            "fp8_compression_tensor_amd/build.py (or __graft_entry__.build())") from e
 
 
+def _table(rows: int, columns: int):
+    """A table of int64, all zeros."""
+    if np is None:
+        raise RuntimeError("grad_norm and adamw need numpy, which is not installed")
+    return np.zeros((rows, columns), dtype=np.int64)
+
+
 def _fill(items, device: int, table, block: int, kinds: int):
     """Begins the int64 table's rows with the list's items (address, alpha's, scale's, number of elements,
     C dtype), and returns the indexes of those that it left out, for the caller to look at."""
@@ -116,7 +127,7 @@ def grad_norm(grads, max_norm: float = math.inf, block: int = 128):
     if not grads:
         raise ValueError("no gradients")
     device = _device_of(grads[0])
-    rows = np.zeros((len(grads), 5), dtype=np.int64)
+    rows = _table(len(grads), 5)
     for i in _fill(grads, device, rows, block, _GRADS):
         rows[i] = _gradient(grads[i], block, device)
     nbytes = lib().tfp8_grad_norm_workspace(len(grads))
@@ -176,12 +187,12 @@ def _adamw_rows(params, grads, copies, block: int, device: int):
     """The table of tfp8_adamw_tensor, the length of the flat states, and the table's address."""
     if _step_rows is None:
         _load()
-    rows = np.zeros((len(params), 12), dtype=np.int64)
+    rows = _table(len(params), 12)
     got = _step_rows(params, grads, copies, device, rows, block)
     if got is not None:
         return rows, *got
     # what is not a plain tensor of the right form: looked at one by one, refused or taken
-    more = np.empty((len(params), 5), dtype=np.int64)
+    more = _table(len(params), 5)
     for i in _fill(params, device, more, block, _PARAMS):
         p = _flat(params[i], device, "a parameter")
         if p.dtype not in _DENSE:

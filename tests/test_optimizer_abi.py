@@ -244,3 +244,27 @@ def test_scales_of_whole_blocks():
     """States of 1000 have seven scales: the two lists of them may not share the seventh."""
     shared = (STATE[0], STATE[1], STATE[2], STATE[1] + 24)
     assert step([put(DENSE, N=896)], state=shared, n=1000) == -6
+
+
+def test_the_package_without_numpy():
+    """Only grad_norm and adamw lay their tables out with numpy: without it they say so, and the rest is there."""
+    import subprocess
+    import sys
+
+    code = """if 1:
+        import sys, warnings
+        warnings.simplefilter("ignore")
+        sys.modules["numpy"] = None
+        import fp8_compression_tensor_amd as tfp8
+        from fp8_compression_tensor_amd import expert_layer, optimizer
+        assert tfp8.lib().tfp8_version() > 0
+        for columns in (5, 12):
+            try:
+                optimizer._table(3, columns)
+            except RuntimeError as e:
+                assert "numpy" in str(e)
+            else:
+                raise AssertionError
+    """
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
