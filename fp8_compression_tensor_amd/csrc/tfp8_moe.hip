@@ -7,9 +7,10 @@
 // registers and into the matrix instructions, with nothing in between but their widening to float16,
 // which is exact.  The rotation is orthogonal, so a row of weights in the rotated basis times x
 // in the rotated basis is the product, and x and the hidden values are rotated instead of the weights.
-// They go into the products as float16, scaled by a power of two for each row so that its largest is
+// They go into the products as float16, scaled by a power of two for each block so that its largest is
 // below 2^15: 11 bits of each value, an eighth of a bfloat16 output's own rounding.  For float32 outputs
-// what that rounds off goes in as a second float16: 22 bits.  Sums are float32.
+// what that rounds off goes in as a second float16: 22 bits.  Sums are float32.  (One power for a whole row
+// would cut off blocks far below its largest value, which count where the weights are small beside that.)
 //
 // Launches, in order:
 //   k_moe_scores  router logits in float64 (a choice hangs on them) and the rotated x
@@ -54,9 +55,8 @@ struct MoeArgs {
   int *where;             // [tokens][experts]: the pair's number, t top_k + .., or -1
   int *ids;               // [pairs]: its expert
   float *gates;           // [pairs]
-  int *x_exp;             // [tokens]: rows are held divided by 2 to this
-  float *h_max;           // [pairs][f / 16]: largest magnitude of h
-  int *h_exp;             // [pairs], as x_exp
+  int *x_exp;             // [tokens][k / block]: blocks are held divided by 2 to this
+  int *h_exp;             // [pairs][f / block], as x_exp
   uint16_t *x_hi, *x_lo;  // [tokens][k], rotated, float16
   float *h;               // [pairs][f]
   uint16_t *h_hi, *h_lo;  // [pairs][f], rotated, float16
@@ -66,22 +66,28 @@ struct MoeArgs {
   int splits;
 };
 
-// By how many powers of two a row is divided whose largest magnitude is m: a rotated value is at most
-// sqrt(B) m, and stays below 2^15.  0 for a row of zeros, and for one that is not finite.
-__device__ __forceinline__ int row_exponent(float m, int block_shift) {
+// By how many powers of two a block is divided whose largest magnitude is m: a rotated value is at most
+// sqrt(B) m, and stays below 2^15.  0 for a block of zeros, and for one that is not finite.
+template <int B>
+__device__ __forceinline__ int block_exponent(float m) {
   if (m == 0.0f || !(m < __builtin_inff())) return 0;
-  return exponent_of(m) + (8 + block_shift) / 2 - 15;  // sqrt(128) < 2^4, sqrt(256) = 2^4, sqrt(512) < 2^5
+  return exponent_of(m) + (B == 512 ? 5 : 4) - 15;  // sqrt(128) < 2^4, sqrt(256) = 2^4, sqrt(512) < 2^5
 }
 
 __device__ __forceinline__ uint16_t bits(_Float16 x) { return __builtin_bit_cast(uint16_t, x); }
 
-// One block of B values, 8 lanes with B / 8 values each, in runs of 8 at 64 g + 8 j: divided by 2^e,
-// rotated and split.  Lane j's results are part lane_perm(j) of each run.
+// One block of B values, 8 lanes with B / 8 values each, in runs of 8 at 64 g + 8 j: divided by a power of
+// two, whose exponent goes to *exp, rotated and split.  Lane j's results are part lane_perm(j) of each run.
 template <int B>
-__device__ __forceinline__ void rotate_values(float (&v)[B / 8], bool rotate, int e, uint16_t *hi,
+__device__ __forceinline__ void rotate_values(float (&v)[B / 8], bool rotate, int *exp, uint16_t *hi,
                                               uint16_t *lo) {
   constexpr int N = B / 8;
   const int j = threadIdx.x & 7;
+  int most = 0;  // as integers: a NaN is larger than all
+#pragma unroll
+  for (int i = 0; i < N; ++i) most = max(most, __float_as_int(fabsf(v[i])));
+  const int e = block_exponent<B>(__int_as_float(group_max_i<8>(most)));
+  if (j == 0) *exp = e;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = scale2(v[i], -e);
   int at = j;
@@ -115,10 +121,10 @@ __device__ __forceinline__ void load_block(float (&v)[B / 8], LOAD load) {
   for (int g = 0; g < B / 64; ++g) load(&v[8 * g], 64 * g + 8 * (threadIdx.x & 7));
 }
 template <int B, class LOAD>
-__device__ __forceinline__ void rotate_block(LOAD load, bool rotate, int e, uint16_t *hi, uint16_t *lo) {
+__device__ __forceinline__ void rotate_block(LOAD load, bool rotate, int *exp, uint16_t *hi, uint16_t *lo) {
   float v[B / 8];
   load_block<B>(v, load);
-  rotate_values<B>(v, rotate, e, hi, lo);
+  rotate_values<B>(v, rotate, exp, hi, lo);
 }
 
 // Eight values from p + at on; wide: 16-byte loads.
@@ -149,13 +155,6 @@ __device__ __forceinline__ void load8(const void *p, int64_t at, bool f32, bool 
   }
 }
 
-// The largest of 64 lanes' magnitudes.
-__device__ __forceinline__ float wave_max(float v) {
-  const int h = group_max_i<32>(__float_as_int(v));
-  const int a = __builtin_amdgcn_readlane(h, 0), b = __builtin_amdgcn_readlane(h, 32);
-  return __int_as_float(a > b ? a : b);
-}
-
 // The first workgroups: a token each, its row rotated.  The others: an expert and up to 8 tokens each,
 // four wavefronts dividing k.
 constexpr int kScoreTokens = 8;
@@ -167,29 +166,13 @@ __global__ __launch_bounds__(kScoreThreads) void k_moe_scores(MoeArgs a) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int W = kScoreThreads / 64;
   if ((int)blockIdx.x < a.tokens) {
-    __shared__ float most[W];
     const int t = blockIdx.x;
     const int64_t row = t * a.ldx;
-    float m = 0.0f;
-    for (int c = 8 * threadIdx.x; c < a.k; c += 8 * kScoreThreads) {
-      float v[8];
-      load8(a.x, row + c, a.x_f32, a.wide, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)  // as integers: a NaN is larger than all
-        m = __int_as_float(max(__float_as_int(m), __float_as_int(fabsf(v[i]))));
-    }
-    m = wave_max(m);
-    if (lane == 0) most[w] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < W; ++i) m = __int_as_float(max(__float_as_int(m), __float_as_int(most[i])));
-    const int e = row_exponent(m, a.block_shift);
-    if (threadIdx.x == 0) a.x_exp[t] = e;
     for (int b = threadIdx.x >> 3; b < a.k / B; b += kScoreThreads / 8) {
       const int64_t to = (int64_t)t * a.k + (int64_t)b * B;
       rotate_block<B>(
-          [&](float *v, int o) { load8(a.x, row + b * B + o, a.x_f32, a.wide, v); }, a.rotate, e,
-          a.x_hi + to, a.out_f32 ? a.x_lo + to : nullptr);
+          [&](float *v, int o) { load8(a.x, row + b * B + o, a.x_f32, a.wide, v); }, a.rotate,
+          a.x_exp + t * (a.k / B) + b, a.x_hi + to, a.out_f32 ? a.x_lo + to : nullptr);
     }
     return;
   }
@@ -384,9 +367,10 @@ __device__ __forceinline__ u32x4 load16(Buffer b, uint32_t lane, int all) {
 // near: the tokens' values lie in LDS.
 template <int NM, int H = 1>
 struct Rows {
-  Buffer codes[NM], alpha[NM], scale[NM], hi, lo;
+  Buffer codes[NM], alpha[NM], scale[NM], hi, lo, exps;
   const uint16_t *near_hi, *near_lo;
-  uint32_t code, factor;   // of its even row; of row lane / 4
+  const int *near_exps;
+  uint32_t code, factor, exp;  // of its even row; of row lane / 4; of token lane / 4
   int places;              // from a row to the next
   uint32_t token[4];       // of its four tokens' values
   int span;
@@ -406,15 +390,19 @@ struct Rows {
   }
   // tokens' rows of values: `row` is that of token n here (any row for none: its sums go nowhere)
   template <bool NEAR = false>
-  __device__ __forceinline__ void set_tokens(const uint16_t *h, const uint16_t *l, int row, int width) {
+  __device__ __forceinline__ void set_tokens(const uint16_t *h, const uint16_t *l, const int *e, int row,
+                                             int width, int blocks) {
     const int lane = threadIdx.x & 63;
     if constexpr (NEAR) {
       near_hi = h;
       near_lo = l;
+      near_exps = e;
     } else {
       hi = buffer_at(h);
       lo = buffer_at(l);
+      exps = buffer_at(e);
     }
+    exp = (uint32_t)__shfl(row, lane >> 2) * blocks * 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t from = (uint32_t)__shfl(row, (lane & 12) + i) * width;
@@ -465,11 +453,15 @@ __device__ __forceinline__ f16x8 widen_codes(uint32_t d0, uint32_t d1) {
   return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// total += the unit's products times the rows' factors, which lane 4 n + `from` holds.
+// total += the unit's products times the rows' factors and 2 to the tokens' exponents, those of row and token n
+// in lane 4 n + `from`.
 template <int NM, bool LO>
-__device__ __forceinline__ void add_unit(f32x4 (&total)[NM], Unit<NM, LO> &p, const float (&f)[NM],
+__device__ __forceinline__ void add_unit(f32x4 (&total)[NM], Unit<NM, LO> &p, const float (&f)[NM], int exp,
                                          int from) {
   const int lane = threadIdx.x & 63, n = lane & 15;
+  int e[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) e[i] = __shfl(exp, (lane & 48) + 4 * i + from);
 #pragma unroll
   for (int k = 0; k < (LO ? 8 : 4); k += 4) {
     exchange<kDppXor1>(p.x[k], p.x[k + 1], lane & 1);
@@ -491,7 +483,7 @@ __device__ __forceinline__ void add_unit(f32x4 (&total)[NM], Unit<NM, LO> &p, co
     }
     const float fu = __shfl(f[m], 4 * n + from);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) total[m][i] = fmaf(sum[i], fu, total[m][i]);
+    for (int i = 0; i < 4; ++i) total[m][i] = fmaf(sum[i], scale2(fu, e[i]), total[m][i]);
   }
 }
 
@@ -505,10 +497,15 @@ __device__ __forceinline__ void sum_units(f32x4 (&total)[NM], const Rows<NM, H> 
   if (u0 >= u1) return;
   constexpr int kDepth = depth_of<NM, LO>();
   float alpha[NM], scale[NM], f[NM];
+  int next_exp, exp;
   const auto load_factors = [&](int u) {  // of units u .. u + 3
     const bool second = H == 2 && threadIdx.x & 32;
     const int mine = u + (int)(threadIdx.x & 3);
     const int b = (min(mine, u1 - 1) + (second ? r.span : 0)) >> shift;
+    if constexpr (NEAR)
+      next_exp = *(const int *)((const char *)r.near_exps + r.exp + 4 * b);
+    else
+      next_exp = (int)__builtin_amdgcn_raw_buffer_load_b32(r.exps, r.exp + 4 * b, 0, 0);
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       alpha[m] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r.alpha[m], r.factor + 4 * b, 0, 0));
@@ -519,6 +516,7 @@ __device__ __forceinline__ void sum_units(f32x4 (&total)[NM], const Rows<NM, H> 
   const auto take_factors = [&] {
 #pragma unroll
     for (int m = 0; m < NM; ++m) f[m] = scale[m] * __builtin_amdgcn_rcpf(alpha[m]);
+    exp = next_exp;
   };
   Unit<NM, LO> p[kDepth];
   load_factors(u0);
@@ -529,13 +527,13 @@ __device__ __forceinline__ void sum_units(f32x4 (&total)[NM], const Rows<NM, H> 
     load_factors(u);
 #pragma unroll
     for (int s = 0; s < kDepth; ++s) {
-      add_unit<NM, LO>(total, p[s], f, s);
+      add_unit<NM, LO>(total, p[s], f, exp, s);
       load_unit<NM, LO, H, NEAR>(p[s], r, min(u + s, u1 - 1));
     }
   }
   take_factors();
 #pragma unroll
-  for (int s = 0; s < kDepth; ++s) add_unit<NM, LO>(total, p[s], f, s);
+  for (int s = 0; s < kDepth; ++s) add_unit<NM, LO>(total, p[s], f, exp, s);
 }
 
 // Which of a set's tokens is number `nth`, from 0 on; -1 past its last.
@@ -603,13 +601,12 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_up(MoeArgs a) {
     const int token = nth_token(s.set, first + n), safe = token < 0 ? __builtin_ctzll(s.set) : token;
     const int of_token = __shfl(s.pair, safe);  // by all lanes: it reads from those past the set, too
     const int pair = token < 0 ? -1 : of_token;
-    const int exponent = a.x_exp[safe];
     f32x4 total[2] = {};
     Rows<2> r;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
       r.set(m, a.up, a.up_alpha, a.up_scale, ((int64_t)s.expert * 2 + m) * a.f + f0, a.k, blocks);
-    r.set_tokens(a.x_hi, a.x_lo, safe, a.k);
+    r.set_tokens(a.x_hi, a.x_lo, a.x_exp, safe, a.k, blocks);
     sum_units<2, LO, 1>(total, r, units * share / kUpParts, units * (share + 1) / kUpParts,
                         a.block_shift);
     if (first) __syncthreads();  // the sums of the tokens before are read
@@ -627,38 +624,20 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_up(MoeArgs a) {
         for (int i = 0; i < 4; ++i) total[m][i] += part[w + k][m][i][lane];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int to = __shfl(pair, 4 * g + i), e = __shfl(exponent, 4 * g + i);
-      const float gate = scale2(total[0][i], e), up = scale2(total[1][i], e);
-      const float h = gate / (1.0f + expf(-gate)) * up;
-      const float most = group_max<16>(fabsf(h));
-      if (to < 0) continue;
-      a.h[(int64_t)to * a.f + f0 + n] = h;
-      if (n == 0) a.h_max[(int64_t)to * (a.f / 16) + f0 / 16] = most;
+      const int to = __shfl(pair, 4 * g + i);
+      const float gate = total[0][i];
+      if (to >= 0) a.h[(int64_t)to * a.f + f0 + n] = gate / (1.0f + expf(-gate)) * total[1][i];
     }
   }
 }
 
-// A row of h: up to 32 blocks a workgroup, each of which finds the row's largest for itself.
+// h, 32 blocks a workgroup.
 constexpr int kRotateThreads = 256;
 template <int B>
-__global__ __launch_bounds__(kRotateThreads) void k_moe_rotate(MoeArgs a, int parts) {
-  constexpr int W = kRotateThreads / 64;
-  __shared__ float most[W];
-  const int pair = blockIdx.x / parts, part = blockIdx.x % parts, tiles = a.f / 16;
-  float m = 0.0f;  // as integers: a NaN is larger than all
-  for (int i = threadIdx.x; i < tiles; i += kRotateThreads)
-    m = __int_as_float(max(__float_as_int(m), __float_as_int(a.h_max[(int64_t)pair * tiles + i])));
-  m = wave_max(m);
-  if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < W; ++i) m = __int_as_float(max(__float_as_int(m), __float_as_int(most[i])));
-  const int e = row_exponent(m, a.block_shift);
-  if (part == 0 && threadIdx.x == 0) a.h_exp[pair] = e;
-  const int b = part * (kRotateThreads / 8) + (threadIdx.x >> 3);
-  if (b >= a.f / B) return;
-  const int64_t at = (int64_t)pair * a.f + (int64_t)b * B;
-  rotate_block<B>([&](float *v, int o) { load8(a.h, at + o, true, true, v); }, a.rotate, e,
+__global__ __launch_bounds__(kRotateThreads) void k_moe_rotate(MoeArgs a) {
+  const int64_t b = (int64_t)blockIdx.x * (kRotateThreads / 8) + (threadIdx.x >> 3), at = b * B;
+  if (at >= (int64_t)a.tokens * a.top_k * a.f) return;
+  rotate_block<B>([&](float *v, int o) { load8(a.h, at + o, true, true, v); }, a.rotate, a.h_exp + b,
                   a.h_hi + at, a.out_f32 ? a.h_lo + at : nullptr);
 }
 
@@ -685,25 +664,10 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeArgs a) {
   __shared__ uint16_t near_hi[NEAR ? kNear : 8], near_lo[NEAR && LO ? kNear : 8];
   __shared__ int near_exp[NEAR ? kNear / 128 : 1];
   if constexpr (NEAR) {
-    const int pairs = a.tokens * a.top_k, per = a.f / B, all = pairs * per, ht = a.f / 16;
-    constexpr int step = 64 * kDownWaves / 8;
-    int b = threadIdx.x >> 3;
-    float v[B / 8];
-    const auto load = [&](float *to, int o) { load8(a.h, (int64_t)b * B + o, true, true, to); };
-    if (b < all) load_block<B>(v, load);  // under way while the rows' largest are found
-    for (int p = threadIdx.x >> 6; p < pairs; p += kDownWaves) {
-      float m = 0.0f;  // as integers: a NaN is larger than all
-      for (int i = threadIdx.x & 63; i < ht; i += 64)
-        m = __int_as_float(max(__float_as_int(m), __float_as_int(a.h_max[(int64_t)p * ht + i])));
-      m = wave_max(m);
-      if ((threadIdx.x & 63) == 0) near_exp[p] = row_exponent(m, a.block_shift);
-    }
-    __syncthreads();
-    while (b < all) {
-      rotate_values<B>(v, a.rotate, near_exp[b / per], near_hi + b * B, LO ? near_lo + b * B : nullptr);
-      b += step;
-      if (b < all) load_block<B>(v, load);
-    }
+    const int all = a.tokens * a.top_k * (a.f / B);
+    for (int b = threadIdx.x >> 3; b < all; b += 64 * kDownWaves / 8)
+      rotate_block<B>([&](float *v, int o) { load8(a.h, (int64_t)b * B + o, true, true, v); }, a.rotate,
+                      near_exp + b, near_hi + b * B, LO ? near_lo + b * B : nullptr);
     __syncthreads();
   }
   __shared__ float sums[kDownWaves][TOKENS][R];
@@ -723,11 +687,6 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeArgs a) {
       const int token = nth_token(s.set, first + (H == 2 ? n & 7 : n));
       const int safe = token < 0 ? __builtin_ctzll(s.set) : token;
       const int pair = __shfl(s.pair, safe);
-      int e;
-      if constexpr (NEAR)
-        e = near_exp[pair];
-      else
-        e = a.h_exp[pair];
       const float gate = a.gates[pair];
       Rows<NM, H> r;
       const int half = (u1 - u0 + H - 1) / H;  // H = 2: the second half ends where the part does
@@ -737,9 +696,9 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeArgs a) {
         r.set(m, a.down, a.down_alpha, a.down_scale, (int64_t)s.expert * a.k + R * tile + 16 * m, a.f,
               blocks);
       if constexpr (NEAR)
-        r.template set_tokens<true>(near_hi, near_lo, pair, a.f);
+        r.template set_tokens<true>(near_hi, near_lo, near_exp, pair, a.f, blocks);
       else
-        r.set_tokens(a.h_hi, a.h_lo, pair, a.f);
+        r.set_tokens(a.h_hi, a.h_lo, a.h_exp, pair, a.f, blocks);
       f32x4 total[NM] = {};
       sum_units<NM, LO, H, NEAR>(total, r, u0, u0 + half, a.block_shift, H == 2 && (u1 - u0) & 1);
       if constexpr (H == 2) {
@@ -749,13 +708,13 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int t = __shfl(token, 4 * g + i), et = __shfl(e, 4 * g + i);
+        const int t = __shfl(token, 4 * g + i);
         const float gt = __shfl(gate, 4 * g + i);
         if (t < 0 || (H == 2 && (g > 1 || n > 7))) continue;
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
           float &to = sums[w][t][16 * m + n];
-          to = fmaf(gt, scale2(total[m][i], et), to);
+          to = fmaf(gt, total[m][i], to);
         }
       }
     }
@@ -835,9 +794,8 @@ int64_t lay_out(MoeArgs &a, char *base, const MoeSizes &s) {
   a.where = (int *)take(s.tokens * s.experts * 4);
   a.ids = (int *)take(pairs * 4);
   a.gates = (float *)take(pairs * 4);
-  a.x_exp = (int *)take(s.tokens * 4);
-  a.h_max = (float *)take(pairs * (s.f / 16) * 4);
-  a.h_exp = (int *)take(pairs * 4);
+  a.x_exp = (int *)take(s.tokens * (s.k / kUnit) * 4);
+  a.h_exp = (int *)take(pairs * (s.f / kUnit) * 4);
   a.x_hi = (uint16_t *)take(s.tokens * s.k * 2);
   a.x_lo = (uint16_t *)take(s.tokens * s.k * 2);
   a.h = (float *)take(pairs * s.f * 4);
@@ -886,8 +844,8 @@ tfp8_status launch_layer(const MoeArgs &a, hipStream_t st) {
   const int rows = down_rows(a.tokens, pairs, a.k);
   const bool near = a.tokens <= kAlone && a.splits == 1 && pairs * a.f <= kNear;  // k_moe_down rotates
   if (!near) {
-    const int parts = (a.f / B + kRotateThreads / 8 - 1) / (kRotateThreads / 8);
-    s = launch(k_moe_rotate<B>, (unsigned)(pairs * parts), kRotateThreads, st, a, parts);
+    const int64_t blocks = pairs * (a.f / B), per = kRotateThreads / 8;
+    s = launch(k_moe_rotate<B>, (unsigned)((blocks + per - 1) / per), kRotateThreads, st, a);
     if (s != TFP8_OK) return s;
   }
   s = launch_down<LO, B>(a, rows, near, st);

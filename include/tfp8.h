@@ -342,8 +342,9 @@ tfp8_status tfp8_adamw(const tfp8_adamw_tensor *tensors, int32_t count, int32_t 
  *   ones' part of the softmax of all;  out[t] = sum over the chosen e of
  *   w[t, e] down_e (silu(W1_e x[t]) * (W3_e x[t])).
  * Logits are float64, other sums float32; x and the hidden values enter the products with 11 bits, for
- * float32 outputs 22, the weights as their codes are.  A token whose logits hold NaN takes some top_k experts all
- * the same, and its row is NaN; other rows do not hang on it.
+ * float32 outputs 22 (no finer than 2^-33 of the largest value of their block), the weights as their codes are,
+ * times s / alpha in float32, which has fewer bits for weights below about 2^-115.  A token whose logits hold
+ * NaN takes some top_k experts all the same, and its row is NaN; other rows do not hang on it.
  *
  * tokens 0 to TFP8_MOE_TOKENS (0: a no-op), experts 1 to TFP8_MOE_EXPERTS, top_k 1 to experts, k and f
  * multiples of block up to 2^20, tokens * top_k * f below 2^29 (TFP8_E_SIZE); block 128, 256 or 512; flags: 0 or the sum of
