@@ -21,9 +21,9 @@
 //   k_moe_join    the sum of the shares
 // For one or two tokens k_moe_up chooses and k_moe_down rotates for itself, where that pays: three launches.
 //
-// Measured, us: one token, 8 of 64 experts of 2048 x 1024 (54 MB) 3.8 + 11 + 8, 23 a call, where a launch
-// that reads 36 MB and first waits for the choice takes 11; 64 tokens, 6 of 64 of 2048 x 1536 (620 MB) scores 6.4, plan
-// 4.8, up 79 (5.3 TB/s), rotate 4.8, down 42 (5.3 TB/s), join 4.8, 139 a call.
+// Measured, us: one token, 8 of 64 experts of 2048 x 1024 (54 MB) 4 + 12 + 8, 23 a call, where a launch
+// that reads 36 MB and first waits for the choice takes 12; 64 tokens, 6 of 64 of 2048 x 1536 (620 MB) scores 6.9, plan
+// 4.8, up 79 (5.4 TB/s), rotate 4.8, down 43 (5.3 TB/s), join 4.9, 140 a call.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -270,8 +270,8 @@ __global__ __launch_bounds__(EXPERTS >= 256 ? 1024 : 256) void k_moe_plan(MoeArg
 }
 
 // Up to this many tokens k_moe_up chooses and k_moe_down rotates (one token, 8 of 64 experts of 2048 x
-// 1024: 23.3 us a call, with launches of their own 26.8; 2 tokens 37.5 and 39.0; 4 tokens, 4 of 16 of
-// 1280 x 640: 35.5 and 33.9).
+// 1024: 23.1 us a call, with launches of their own 25.4; 2 tokens 36.1 and 38.0; 2 tokens, 4 of 16 of
+// 1280 x 640: 22.5 and 25.1; for 4 tokens it was 35.5 and 33.9).
 constexpr int kAlone = 2;
 
 // The same choice by a workgroup of four wavefronts for itself, for one or two tokens and up to 64 experts.
@@ -753,15 +753,16 @@ constexpr int64_t kMostHidden = (int64_t)1 << 29;  // of all pairs: k_moe_up has
 // 8 rows where that fills the compute units (one token, 8 of 64 experts of 2048 x 1024: 24.1 us a call
 // against 25.1), unless the wavefronts have many slots each, which then take as long to look up as to read
 // (8 tokens, 6 of 64 of 2048 x 1408: 94 against 86).  32 rows read a token's values half as often (48
-// tokens, 4 of 16 of 2560 x 1024: 62 against 65; 64 tokens, 2 of 8 of 4096 x 2048: 77 against 71).
+// tokens, 4 of 16 of 2560 x 1024: 64 against 69; 36 tokens, 7 of 10 of 4864 x 3200: 267 against 306; but 64
+// tokens, 2 of 8 of 4096 x 2048: 101 against 92).
 int down_rows(int64_t tokens, int64_t pairs, int64_t k) {
   if (tokens <= 8 && pairs <= 16 && k < 4096) return 8;
   return pairs >= 192 ? 32 : 16;
 }
 // Experts are shared out until the compute units are full, as long as each wavefront keeps a slot; and to more
-// than half of them where it keeps 8 units of a part of one (52 tokens, 5 of 16 of 384 x 14336, float32: 498 us
-// a call without that, 220 with; 18 tokens, 4 of 8 of 768 x 2688: 49 and 45; but to all of them 3 tokens, 4 of 26 of 1536
-// x 2048: 50 and 55).
+// than half of them where it keeps 8 units of a part of one (52 tokens, 5 of 16 of 384 x 14336, float32: 546 us
+// a call without that, 228 with; 18 tokens, 4 of 8 of 768 x 2688: 43 and 38; but to all of them 3 tokens, 4 of 26 of 1536
+// x 2048: 44 and 49).
 int down_splits(int64_t tokens, int64_t pairs, int64_t experts, int64_t k, int64_t f) {
   const int64_t tiles = k / down_rows(tokens, pairs, k), slots = std::min(pairs, experts);
   const int64_t units = f / kUnit;

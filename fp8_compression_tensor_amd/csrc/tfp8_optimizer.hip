@@ -47,8 +47,8 @@ __device__ __forceinline__ int entry_of(const E *e, int count, int64_t x) {
 // The norm.  A workgroup takes units of 16 KB (kLoads 16-byte loads a lane, all under way at once),
 // every gridDim.x-th of the launch's, and writes one float64 partial sum; k_norm_finish adds the
 // partial sums in order.  No atomics: the order hangs on the sizes alone, so that repeated calls agree
-// bit for bit.  Bound by memory: 451 MB of bfloat16 in 67 us (6.8 TB/s; part of it lies in the 256 MB
-// cache), 285 MB of codes in 48 us (5.9).  Units of 8192 elements, 1024 or 2048 workgroups and 4 or 6
+// bit for bit.  Bound by memory: 451 MB of bfloat16 in 69 us (6.5 TB/s; part of it lies in the 256 MB
+// cache), 285 MB of codes in 46 us (6.2).  Units of 8192 elements, 1024 or 2048 workgroups and 4 or 6
 // wavefronts a SIMD are within 3% of each other.  The finish takes 4 us, most of it a launch's own time (its
 // four loads one after the other: 0.4 more).
 

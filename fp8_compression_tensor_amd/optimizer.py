@@ -245,7 +245,8 @@ def adamw(params, grads, state, lr, betas=(0.9, 0.999), eps: float = 1e-8,
       into a graph takes their values at each replay.
     scale: None, or a float32 tensor of one element that multiplies the gradients (grad_norm's).  Where
       it is infinite or NaN, the step is left out: params and copies stay as they were, and the new
-      state is the old one.
+      state is the old one.  Such a step is not to count: t = steps + torch.isfinite(scale), with the
+      number of steps taken as a tensor, does without the host.
     copies: None, or for each parameter None, a bfloat16 tensor (p' to nearest even) or (codes, alpha,
       scale), p' compressed in the same blocks with target 1; written once more at each step.
     seed: of the random bits; they hang on seed, step and position alone.

@@ -252,7 +252,7 @@ tfp8_status tfp8_matmul_grouped_t(const uint8_t *a_codes, int64_t a_ld, const fl
  *
  * A gradient is dense (bfloat16 or float32, any n) or compressed (TFP8_CODES: E4M3 codes[n], alpha and
  * scale[n / block], as tfp8_compress or tfp8_accumulate wrote them with flags = 0; n a multiple of
- * block).  The arrays of tensors are HOST memory, read before the call returns; what they point to
+ * block; s / alpha is float32, which has fewer bits for values below about 2^-115).  The arrays of tensors are HOST memory, read before the call returns; what they point to
  * is device memory.  Rules in common: 0 <= count <= 2^24 and 0 <= n <= TFP8_MAX_N for each tensor
  * (TFP8_E_SIZE); block 64, 128, 256 or 512; data, params, copies and states 16-byte aligned, scales 4.
  * A tensor with n = 0 is left out and its pointers are not examined. */
@@ -304,7 +304,8 @@ typedef struct {
  * Arithmetic is float32; the factors of a step are float64, rounded once.  A grad_scale that is infinite or
  * NaN leaves the step out: params and copies stay as they were, and the new states are the old ones.
  * States of 32 bits hold v' itself: where sqrt(1 - beta2) |g| is below 2^-63 it has fewer bits, below 2^-75
- * none, so that an eps below about 2^-70 does not hold such a step back.
+ * none, so that an eps below about 2^-70 does not hold such a step back, and from 2^64 on it is infinite, and
+ * the element stays as it is from there on.  States of 8 bits hold the root, and reach from 2^-100 to 2^126.
  *
  * States are flat, and go from m, v to m_out, v_out: each of these four and their scales is exactly
  * its input (in place) or apart from all else.  Element i of a tensor has its states at start + i, start a multiple of block, the
